@@ -1,4 +1,4 @@
-"""Python binding of libnvfp4 (include/nvfp4.h): argument marshalling only.
+"""Python binding of libnvfp4 (include/*.h): argument marshalling only.
 
 Each function has the name and the argument order of its C entry point.  Tensor
 arguments may be torch tensors (their data_ptr is passed), raw integer device
@@ -22,7 +22,10 @@ NVFP4_ROW_1D, NVFP4_COL_1D, NVFP4_TILE_2D = 0, 1, 2
 EXPORTED = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_quantize_row_rht", "nvfp4_gemm",
             "nvfp4_gemm_noalloc", "nvfp4_gemm_bf16", "nvfp4_dequantize", "nvfp4_gemm_workspace_size",
             "nvfp4_set_quantize_passes", "nvfp4_set_sync_spin_limit", "nvfp4_single_pass_stats",
-            "nvfp4_status_str", "mxfp4_quantize", "mxfp4_gemm")
+            "nvfp4_status_str", "mxfp4_quantize", "mxfp4_gemm", "nvfp4_dropout", "nvfp4_rms_norm",
+            "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_size",
+            "nvfp4_linear_cross_entropy", "nvfp4_linear_cross_entropy_backward",
+            "nvfp4_linear_cross_entropy_workspace_size")
 
 _lib = None
 
@@ -81,6 +84,23 @@ def load_library():
     L.nvfp4_set_sync_spin_limit.restype = i32
     L.nvfp4_single_pass_stats.argtypes = [ctypes.POINTER(i64), ctypes.POINTER(i64)]
     L.nvfp4_single_pass_stats.restype = i32
+    L.nvfp4_dropout.argtypes = [vp, i32, i64, i64, i64, f32, u64, vp, i64, vp]
+    L.nvfp4_dropout.restype = i32
+    L.nvfp4_rms_norm.argtypes = [vp, vp, i32, i64, i64, i64, i64, vp, i32, f32, f32, u64, vp, i64, vp,
+                                 i64, vp, vp, vp, vp]
+    L.nvfp4_rms_norm.restype = i32
+    L.nvfp4_rms_norm_backward.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i64, vp, i32, vp, f32,
+                                          u64, vp, i64, vp, i64, vp, vp, i64, vp]
+    L.nvfp4_rms_norm_backward.restype = i32
+    L.nvfp4_rms_norm_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    L.nvfp4_rms_norm_backward_workspace_size.restype = i32
+    L.nvfp4_linear_cross_entropy.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]
+    L.nvfp4_linear_cross_entropy.restype = i32
+    L.nvfp4_linear_cross_entropy_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                                      i64, vp, i32, i64, f32, vp, i64, vp]
+    L.nvfp4_linear_cross_entropy_backward.restype = i32
+    L.nvfp4_linear_cross_entropy_workspace_size.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
+    L.nvfp4_linear_cross_entropy_workspace_size.restype = i32
     L.nvfp4_status_str.argtypes = [i32]
     L.nvfp4_status_str.restype = ctypes.c_char_p
     _lib = L
@@ -106,6 +126,15 @@ def _stream(stream):
 
 def nvfp4_status_str(status: int) -> str:
     return load_library().nvfp4_status_str(status).decode()
+
+
+def _bytes(workspace, workspace_bytes) -> int:
+    """`workspace_bytes=None` takes the size of a torch-tensor workspace (0 for
+    a raw address or None)."""
+    if workspace_bytes is None:
+        return 0 if workspace is None or isinstance(workspace, int) else \
+            workspace.numel() * workspace.element_size()
+    return int(workspace_bytes)
 
 
 def _check(fn: str, status: int, raise_on_error: bool) -> int:
@@ -234,3 +263,64 @@ def nvfp4_single_pass_stats() -> tuple[int, int]:
     _check("nvfp4_single_pass_stats",
            load_library().nvfp4_single_pass_stats(ctypes.byref(n), ctypes.byref(g)), True)
     return n.value, g.value
+
+
+def nvfp4_dropout(x, dt, rows, cols, ld_x, p, seed, y, ld_y, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_dropout(_addr(x), dt, rows, cols, ld_x, float(p), seed & (2 ** 64 - 1),
+                                      _addr(y), ld_y, _stream(stream))
+    return _check("nvfp4_dropout", st, raise_on_error)
+
+
+def nvfp4_rms_norm(x, residual, dt, rows, cols, ld_x, ld_r, gamma, gamma_dt, eps, p, seed, h, ld_h, y,
+                   ld_y, codes, scales, rstd, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_rms_norm(
+        _addr(x), _addr(residual), dt, rows, cols, ld_x, ld_r, _addr(gamma), gamma_dt, float(eps),
+        float(p), seed & (2 ** 64 - 1), _addr(h), ld_h, _addr(y), ld_y, _addr(codes), _addr(scales),
+        _addr(rstd), _stream(stream))
+    return _check("nvfp4_rms_norm", st, raise_on_error)
+
+
+def nvfp4_rms_norm_backward_workspace_size(rows, cols) -> int:
+    """Workspace bytes of nvfp4_rms_norm_backward with a dgamma."""
+    out = ctypes.c_int64(0)
+    _check("nvfp4_rms_norm_backward_workspace_size",
+           load_library().nvfp4_rms_norm_backward_workspace_size(rows, cols, ctypes.byref(out)), True)
+    return out.value
+
+
+def nvfp4_rms_norm_backward(dy, dh, h, dt, rows, cols, ld_dy, ld_dh, ld_h, gamma, gamma_dt, rstd, p,
+                            seed, dx, ld_dx, dresidual, ld_dr, dgamma, workspace=None,
+                            workspace_bytes=None, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_rms_norm_backward(
+        _addr(dy), _addr(dh), _addr(h), dt, rows, cols, ld_dy, ld_dh, ld_h, _addr(gamma), gamma_dt,
+        _addr(rstd), float(p), seed & (2 ** 64 - 1), _addr(dx), ld_dx, _addr(dresidual), ld_dr,
+        _addr(dgamma), _addr(workspace), _bytes(workspace, workspace_bytes), _stream(stream))
+    return _check("nvfp4_rms_norm_backward", st, raise_on_error)
+
+
+def nvfp4_linear_cross_entropy_workspace_size(T, V, H, train) -> int:
+    """Workspace bytes of the linear cross entropy: its forward alone, or
+    (train true) either direction."""
+    out = ctypes.c_int64(0)
+    _check("nvfp4_linear_cross_entropy_workspace_size",
+           load_library().nvfp4_linear_cross_entropy_workspace_size(T, V, H, int(bool(train)),
+                                                                    ctypes.byref(out)), True)
+    return out.value
+
+
+def nvfp4_linear_cross_entropy(T, V, H, x, ld_x, w, ld_w, labels, loss, lse, workspace=None,
+                               workspace_bytes=None, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_linear_cross_entropy(
+        T, V, H, _addr(x), ld_x, _addr(w), ld_w, _addr(labels), _addr(loss), _addr(lse),
+        _addr(workspace), _bytes(workspace, workspace_bytes), _stream(stream))
+    return _check("nvfp4_linear_cross_entropy", st, raise_on_error)
+
+
+def nvfp4_linear_cross_entropy_backward(T, V, H, x, ld_x, w, ld_w, labels, lse, dloss, dx, ld_dx, dw,
+                                        dw_dt, ld_dw, beta, workspace=None, workspace_bytes=None,
+                                        stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_linear_cross_entropy_backward(
+        T, V, H, _addr(x), ld_x, _addr(w), ld_w, _addr(labels), _addr(lse), _addr(dloss), _addr(dx),
+        ld_dx, _addr(dw), dw_dt, ld_dw, float(beta), _addr(workspace),
+        _bytes(workspace, workspace_bytes), _stream(stream))
+    return _check("nvfp4_linear_cross_entropy_backward", st, raise_on_error)
