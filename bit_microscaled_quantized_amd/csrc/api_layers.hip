@@ -26,6 +26,9 @@ bool ld_ok(const void* p, int64_t ld, int64_t rows, int64_t cols) {
   return ld >= cols && ld < (int64_t(1) << 40) && (rows == 0 || ld <= (int64_t(1) << 40) / rows);
 }
 
+// 256 rows of an operand stay within 32-bit byte offsets.
+constexpr int64_t kMaxLd = int64_t(1) << 22;
+
 nvfp4_status done(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_EHIP; }
 
 nvfp4_status check_loss(int64_t T, int64_t V, int64_t H, const void* x, int64_t ld_x, const void* w, int64_t ld_w,
@@ -37,7 +40,7 @@ nvfp4_status check_loss(int64_t T, int64_t V, int64_t H, const void* x, int64_t 
   if (st != NVFP4_OK) return st;
   if (need > 0 && workspace == nullptr) return NVFP4_EINVAL;
   if (workspace_bytes < need) return NVFP4_ESHAPE;
-  if (ld_x < H || ld_w < H || ld_x >= (int64_t(1) << 32) || ld_w >= (int64_t(1) << 32)) return NVFP4_ESHAPE;
+  if (ld_x < H || ld_w < H || ld_x >= kMaxLd || ld_w >= kMaxLd) return NVFP4_ESHAPE;
   if (!aligned(x, 16) || !aligned(w, 16) || ld_x % 8 != 0 || ld_w % 8 != 0 || !aligned(labels, 8) ||
       !aligned(lse, 4) || !aligned(workspace, 16))
     return NVFP4_EALIGN;
@@ -117,7 +120,7 @@ nvfp4_status nvfp4_rms_norm_backward(const void* dy, const void* dh, const void*
 
 nvfp4_status nvfp4_linear_cross_entropy_workspace_size(int64_t T, int64_t V, int64_t H, int train, int64_t* bytes) {
   if (bytes == nullptr) return NVFP4_EINVAL;
-  if (T < 0 || T >= (int64_t(1) << 22) || V <= 0 || H <= 0 || V >= (int64_t(1) << 24) || H >= (int64_t(1) << 22) ||
+  if (T < 0 || T >= (int64_t(1) << 22) || V <= 0 || H <= 0 || V >= (int64_t(1) << 24) || H >= kMaxLd ||
       H % 8 != 0)
     return NVFP4_ESHAPE;
   *bytes = T == 0 ? 0 : nvfp4::linear_ce_workspace(T, V, H, train != 0);
@@ -145,8 +148,7 @@ nvfp4_status nvfp4_linear_cross_entropy_backward(int64_t T, int64_t V, int64_t H
   if (T > 0 && (dloss == nullptr || (dx == nullptr && dw == nullptr))) return NVFP4_EINVAL;
   const nvfp4_status st = check_loss(T, V, H, x, ld_x, w, ld_w, labels, lse, workspace, workspace_bytes, true);
   if (st != NVFP4_OK) return st;
-  const int64_t big = int64_t(1) << 32;
-  if ((dx != nullptr && (ld_dx < H || ld_dx >= big)) || (dw != nullptr && (ld_dw < H || ld_dw >= big)))
+  if ((dx != nullptr && (ld_dx < H || ld_dx >= kMaxLd)) || (dw != nullptr && (ld_dw < H || ld_dw >= kMaxLd)))
     return NVFP4_ESHAPE;
   if (!aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16) || (dx != nullptr && ld_dx % 8 != 0) ||
       (dw != nullptr && ld_dw % (dw_dt == NVFP4_BF16 ? 8 : 4) != 0))

@@ -101,7 +101,7 @@ nvfp4_status nvfp4_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, 
  * tiles and never stored.
  *   x [T][ld_x], w [V][ld_w] BF16, 16-byte aligned, ld a multiple of 8;
  *   labels [T] int64; loss, lse [T] FP32.  H a positive multiple of 8, V >= 1,
- *   T and H < 2^22, V < 2^24.
+ *   T, H and every ld < 2^22, V < 2^24.
  *   workspace: at least nvfp4_linear_cross_entropy_workspace_size(T, V, H, 0)
  *   bytes, 16-byte aligned, in use until the call's work on `stream` completes.
  *   Fewer bytes: NVFP4_ESHAPE.
