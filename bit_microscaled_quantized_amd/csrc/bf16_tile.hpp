@@ -3,12 +3,17 @@
 // for operands that hold K along their rows (element (m, k) at p[m * ld + k]) or
 // down their columns (KMAJOR, element (m, k) at p[k * ld + m]).
 //
-// 512 threads = 8 waves (two per SIMD, so that one wave's LDS reads and waits
-// overlap the other's matrix instructions) in a 2 x 4 grid; wave tile 128 x 64 =
-// 4 x 2 MFMA tiles of 32 x 32 x 16 (128 FP32 accumulators a lane).  A stage is
-// 64 values of k: 32 KB per operand, fetched straight into LDS one stage ahead
-// (two buffers, 128 KB), 16 bytes per lane, so that no registers hold data in
-// flight.
+// 256 threads = 4 waves, one per SIMD, in a 2 x 2 grid; wave tile 128 x 128 =
+// 4 x 4 MFMA tiles of 32 x 32 x 16 (256 FP32 accumulators a lane).  The chip's
+// power limits this product, not its matrix rate (at full occupation of the
+// matrix cores by random data the clock falls from 2.4 to 1.8 GHz), so what
+// counts is energy per product: the square wave tile reads a third less from LDS
+// than 8 waves of 128 x 64 (32768 x 8192 x 5120: 1.98 ms against 2.20, 1386
+// against 1250 TFLOP/s).  A stage is 64 values of k: 32 KB per operand, fetched
+// straight into LDS (two buffers, 128 KB), 16 bytes per lane in whole 128-byte
+// lines (stages of 32 values, twice as many in flight, run their 64-byte requests
+// at more energy: 2.25 ms).  With one wave per SIMD nothing else hides a wait, so
+// the reads and fetches are placed between the matrix instructions by hand.
 //
 // LDS layouts, both free of bank conflicts (64 banks of 4 bytes):
 //   * K along rows: 256 rows of 128 bytes; the 16-byte chunk c of row r lies in
@@ -50,7 +55,7 @@ constexpr int TILE_K = 64;              // values of k per stage
 constexpr int TILE_OPERAND = 32 * 1024;  // bytes of an operand's stage
 constexpr int TILE_STAGE = 2 * TILE_OPERAND;
 constexpr int TILE_LDS = 2 * TILE_STAGE;
-constexpr int TILE_THREADS = 512;
+constexpr int TILE_THREADS = 256;
 
 // An operand of a tile: its first element (m = the tile's first row, k = 0),
 // leading dimension, and rows from there on (at least one; KMAJOR: rounded up to
@@ -63,57 +68,61 @@ struct TileOperand {
   int krows;
 };
 
-// Fetch offsets (bytes) of a lane's four 16-byte loads of a stage.
+// Fetch offsets (bytes) of a lane's eight 16-byte loads of a stage: load j of a
+// wave fills bytes 1024 (8 wave + j) .. of the operand's stage.
 template <bool KMAJOR>
 struct TileFetch {
-  uint32_t off[4];
+  uint32_t off[8];
   __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane, int krows) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < 8; j++) {
       if constexpr (!KMAJOR) {
-        const int r = 8 * (4 * wave + j) + (lane >> 3);
+        const int r = 8 * (8 * wave + j) + (lane >> 3);
         off[j] = (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
       } else {
-        const int k = 2 * (4 * wave + j) + (lane >> 5);
+        const int k = 2 * (8 * wave + j) + (lane >> 5);
         const int g = (lane & 31) ^ ((k & 3) << 2);
         off[j] = (uint32_t)min(k, krows - 1) * (o.ld * 2) + 2 * min(8 * g, o.rows - 8);
       }
     }
   }
+  // load j of stage kt
+  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int j) const {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
+                          (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
+    uint32_t v = off[j];
+    asm volatile("" : "+v"(v));  // a 32-bit offset register beside the scalar base
+    __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (8 * wave + j) * 1024), 16, 0, 0);
+  }
 };
 
+// The last stage, K not a multiple of 64: zeros past K (K along rows), or rows up
+// to the operand's last (KMAJOR).
 template <bool KMAJOR>
-__device__ __forceinline__ void tile_issue(const TileOperand& o, const TileFetch<KMAJOR>& f, int kt, uint8_t* st,
-                                           int wave) {
-  const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
-                        (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    uint32_t v = f.off[j];
-    asm volatile("" : "+v"(v));  // a 32-bit offset register beside the scalar base
-    __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (4 * wave + j) * 1024), 16, 0, 0);
-  }
-}
-
-// The last stage of an operand with K along its rows, K not a multiple of 64:
-// chunks past K are zeros.
 __device__ __forceinline__ void tile_last(const TileOperand& o, int kt, int K, uint8_t* st, int wave, int lane) {
-  const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) + (int64_t)kt * TILE_K * 2;
+  if constexpr (KMAJOR) {
+    TileFetch<true> f;
+    f.init(o, wave, lane, o.krows - kt * TILE_K);
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int r = 8 * (4 * wave + j) + (lane >> 3);
-    const int c = (lane & 7) ^ ((r >> 1) & 7);
-    u32x4_t v = {0, 0, 0, 0};
-    if (kt * TILE_K + 8 * c < K)
-      v = *reinterpret_cast<const u32x4_t*>(base + (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * c);
-    *reinterpret_cast<u32x4_t*>(st + (4 * wave + j) * 1024 + lane * 16) = v;
+    for (int j = 0; j < 8; j++) f.issue(o, kt, st, wave, j);
+  } else {
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) + (int64_t)kt * TILE_K * 2;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const int r = 8 * (8 * wave + j) + (lane >> 3);
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      u32x4_t v = {0, 0, 0, 0};
+      if (kt * TILE_K + 8 * c < K)
+        v = *reinterpret_cast<const u32x4_t*>(base + (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * c);
+      *reinterpret_cast<u32x4_t*>(st + (8 * wave + j) * 1024 + lane * 16) = v;
+    }
   }
 }
 
-// Fragments of TILES MFMA tiles from row `first` of the operand's stage.
-template <bool KMAJOR, int TILES>
+// Fragments of the wave's four MFMA tiles from row `first` of the operand's stage.
+template <bool KMAJOR>
 struct TileFrag {
-  uint32_t at[KMAJOR ? TILES : 1];
+  uint32_t at[KMAJOR ? 4 : 1];
   uint32_t x;
   __device__ __forceinline__ void init(int first, int lane) {
     if constexpr (!KMAJOR) {
@@ -123,7 +132,7 @@ struct TileFrag {
       const int b = lane >> 4, i = lane & 15;
       x = 0;
 #pragma unroll
-      for (int t = 0; t < TILES; t++) {
+      for (int t = 0; t < 4; t++) {
         const int g = (((first >> 3) + 4 * t) ^ ((i >> 2) << 2)) + 2 * (b & 1) + ((i & 3) >> 1);
         at[t] = (uint32_t)(8 * (b >> 1) + (i >> 2)) * 512 + g * 16 + (i & 1) * 8;
       }
@@ -141,12 +150,12 @@ struct TileFrag {
   }
 };
 
-// acc = the product over the stages kt0 .. kt1 - 1 (at least one) of K values
-// of k.  All waves of the workgroup take part; the caller's LDS stages are free
-// again after its next barrier.
+// acc = the product over the stages kt0 .. kt1 - 1 of K values of k.  All waves
+// of the workgroup take part; the caller's LDS stages are free again after its
+// next barrier.
 template <bool AMAJ, bool BMAJ>
 __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOperand& b, int K, int kt0, int kt1,
-                                             uint8_t* lds, floatx16 (&acc)[4][2]) {
+                                             uint8_t* lds, floatx16 (&acc)[4][4]) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5;
@@ -154,81 +163,142 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
   TileFetch<BMAJ> fb;
   fa.init(a, wave, lane, TILE_K);
   fb.init(b, wave, lane, TILE_K);
-  TileFrag<AMAJ, 4> ra;
-  TileFrag<BMAJ, 2> rb;
-  ra.init((wave >> 2) * 128, lane);
-  rb.init((wave & 3) * 64, lane);
-  const bool ragged = (K & (TILE_K - 1)) != 0;
-  const int last = (K + TILE_K - 1) / TILE_K - 1;
-  // fetch of stage kt; the stage that ends past K by its own rule
-  auto issue = [&](int kt, uint8_t* st) {
-    if (ragged && kt == last) {
-      if constexpr (AMAJ) {
-        TileFetch<AMAJ> f;
-        f.init(a, wave, lane, a.krows - kt * TILE_K);
-        tile_issue<AMAJ>(a, f, kt, st, wave);
-      } else {
-        tile_last(a, kt, K, st, wave, lane);
-      }
-      if constexpr (BMAJ) {
-        TileFetch<BMAJ> f;
-        f.init(b, wave, lane, b.krows - kt * TILE_K);
-        tile_issue<BMAJ>(b, f, kt, st + TILE_OPERAND, wave);
-      } else {
-        tile_last(b, kt, K, st + TILE_OPERAND, wave, lane);
-      }
-      return;
-    }
-    tile_issue<AMAJ>(a, fa, kt, st, wave);
-    tile_issue<BMAJ>(b, fb, kt, st + TILE_OPERAND, wave);
-  };
+  TileFrag<AMAJ> ra;
+  TileFrag<BMAJ> rb;
+  ra.init((wave >> 1) * 128, lane);
+  rb.init((wave & 1) * 128, lane);
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+    for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+  bf16x8_t va[2][4], vb[2][4];
 
-  bf16x8_t va[2][4], vb[2][2];
-  auto read = [&](const uint8_t* st, int s, int q) {
+  // The stage that ends past K, and one more where the rest is odd, go first,
+  // each fetched and multiplied by itself.
+  auto alone = [&](int kt, bool ragged) {
+    if (ragged) {
+      tile_last<AMAJ>(a, kt, K, lds, wave, lane);
+      tile_last<BMAJ>(b, kt, K, lds + TILE_OPERAND, wave, lane);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++) va[q][i] = ra.read(st, i, s, h);
-#pragma unroll
-    for (int j = 0; j < 2; j++) vb[q][j] = rb.read(st + TILE_OPERAND, j, s, h);
-  };
-  auto mma = [&](int q) {
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int j = 0; j < 2; j++)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q][i], vb[q][j], acc[i][j], 0, 0, 0);
-  };
-
-  issue(kt0, lds);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  read(lds, 0, 0);
-  // One stage.  The two buffers are disjoint; restrict lets the compiler see
-  // that the reads of cur do not wait for the fetch into nxt.
-  auto stage = [&](int kt, const uint8_t* __restrict__ cur, uint8_t* __restrict__ nxt) {
-    const bool more = kt + 1 < kt1;
-    if (more) issue(kt + 1, nxt);
-#pragma unroll
-    for (int s = 0; s < 3; s++) {
-      read(cur, s + 1, (s + 1) & 1);
-      mma(s & 1);
+      for (int j = 0; j < 8; j++) {
+        fa.issue(a, kt, lds, wave, j);
+        fb.issue(b, kt, lds + TILE_OPERAND, wave, j);
+      }
     }
-    // every wave's reads of cur are complete and its part of nxt has landed
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (more) read(nxt, 0, 0);
-    mma(1);
+#pragma unroll 1
+    for (int s = 0; s < 4; s++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        va[0][i] = ra.read(lds, i, s, h);
+        vb[0][i] = rb.read(lds + TILE_OPERAND, i, s, h);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[0][i], vb[0][j], acc[i][j], 0, 0, 0);
+    }
+    __syncthreads();
   };
-  for (int kt = kt0; kt < kt1; kt++) {
-    uint8_t* cur = lds + ((kt - kt0) & 1) * TILE_STAGE;
-    uint8_t* nxt = lds + ((kt - kt0 + 1) & 1) * TILE_STAGE;
-    stage(kt, cur, nxt);
+  bool ragged = (K & (TILE_K - 1)) != 0 && kt1 * TILE_K > K;
+  int first = kt0, end = ragged ? kt1 - 1 : kt1;
+  const bool odd = ((end - first) & 1) != 0;
+  if (ragged || odd) {
+#pragma unroll 1
+    for (int pass = 0; pass < 2; pass++) {
+      if (pass == 0 ? ragged : odd) alone(pass == 0 ? end : first, pass == 0);
+    }
+    if (odd) first++;
   }
+  if (first == end) return;
+
+  // A stage is four steps of 16 values of k, 16 matrix instructions each.  Each
+  // step first reads the next step's fragments, two reads after each of its first
+  // four matrix instructions (of the next stage, after the barrier that ends a
+  // stage, in the last step).  A stage's loads are issued between the matrix
+  // instructions of two steps: half of them as soon as their buffer is free,
+  // after that barrier, half in the step after.  (All at once they keep the wave
+  // from the matrix core until the address unit has taken them; later, they have
+  // not landed when the stage ends.)  The last two stages' loads are clamped to
+  // the last stage, so that every stage is the same code; what they fetch is not
+  // read.  The schedule barriers hold the order as written.
+#define TILE_FENCE __builtin_amdgcn_sched_barrier(0)
+#define TILE_READ(st, s, q, x)                                     \
+  do {                                                             \
+    if ((x) == 0)                                                  \
+      va[q][0] = ra.read(st, 0, s, h);                             \
+    else if ((x) < 5)                                              \
+      vb[q][(x)-1] = rb.read((st) + TILE_OPERAND, (x)-1, s, h);    \
+    else                                                           \
+      va[q][(x)-4] = ra.read(st, (x)-4, s, h);                     \
+  } while (0)
+#define TILE_LOAD(kt, st, x)                              \
+  do {                                                    \
+    if ((x)&1)                                            \
+      fb.issue(b, kt, (st) + TILE_OPERAND, wave, (x) >> 1); \
+    else                                                  \
+      fa.issue(a, kt, st, wave, (x) >> 1);                \
+  } while (0)
+  // fragments q in use; the next step's from step rs of rst; loads x0 .. x0 + 7 of stage kt into dst
+#define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                       \
+  do {                                                                                                  \
+    _Pragma("unroll") for (int m = 0; m < 16; m++) {                                                    \
+      acc[m >> 2][m & 3] =                                                                              \
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q][m >> 2], vb[q][m & 3], acc[m >> 2][m & 3], 0, 0, 0); \
+      TILE_FENCE;                                                                                       \
+      if (m < 4) {                                                                                      \
+        TILE_READ(rst, rs, 1 - (q), 2 * m);                                                             \
+        TILE_READ(rst, rs, 1 - (q), 2 * m + 1);                                                         \
+      } else if (m < 12) {                                                                              \
+        if (fetch) TILE_LOAD(kt, dst, (x0) + m - 4);                                                    \
+      }                                                                                                 \
+      TILE_FENCE;                                                                                       \
+    }                                                                                                   \
+  } while (0)
+  // the wait: this wave's reads of cur are complete and its part of nxt has landed
+#define TILE_STAGE_OF(kt, cur, nxt)                               \
+  do {                                                            \
+    const int k1 = min((kt) + 1, end - 1), k2 = min((kt) + 2, end - 1); \
+    TILE_STEP(0, cur, 1, true, k1, nxt, 8);                       \
+    TILE_STEP(1, cur, 2, false, 0, nxt, 0);                       \
+    TILE_STEP(0, cur, 3, false, 0, nxt, 0);                       \
+    asm volatile("" ::: "memory");                                \
+    __builtin_amdgcn_s_waitcnt(0x70); /* vmcnt(0) lgkmcnt(0) */   \
+    TILE_FENCE;                                                   \
+    __builtin_amdgcn_s_barrier();                                 \
+    TILE_FENCE;                                                   \
+    asm volatile("" ::: "memory");                                \
+    TILE_STEP(1, nxt, 0, true, k2, cur, 0);                       \
+  } while (0)
+#pragma unroll
+  for (int x = 0; x < 16; x++) TILE_LOAD(first, lds, x);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 8; x++) TILE_READ(lds, 0, 0, x);
+#pragma unroll
+  for (int x = 0; x < 8; x++) TILE_LOAD(first + 1, lds + TILE_STAGE, x);
+  // restrict (on arguments that the compiler cannot replace by their values)
+  // lets it see that reads of one buffer do not wait for the fetch into the other
+  auto pair = [&](int kt, uint8_t* __restrict__ b0, uint8_t* __restrict__ b1) {
+    TILE_STAGE_OF(kt, b0, b1);
+    TILE_STAGE_OF(kt + 1, b1, b0);
+  };
+  uint32_t o0 = 0, o1 = TILE_STAGE;
+  asm volatile("" : "+s"(o0), "+s"(o1));
+  for (int kt = first; kt < end; kt += 2) pair(kt, lds + o0, lds + o1);
+  // the clamped loads have landed before the caller uses the LDS
+  __builtin_amdgcn_s_waitcnt(0);
+#undef TILE_STAGE_OF
+#undef TILE_STEP
+#undef TILE_LOAD
+#undef TILE_READ
+#undef TILE_FENCE
 }
 
 // Tile (pm, pn) of workgroup bid in a grid of num_m x num_n tiles.  Workgroups

@@ -11,7 +11,7 @@
 //
 // Every product has its output's contiguous dimension as the tile's rows m, so a
 // lane holds four consecutive values of an output row (or 64 logits of each of
-// two tokens): the operands are fetched in whichever orientation they lie in
+// four tokens): the operands are fetched in whichever orientation they lie in
 // memory, and nothing is transposed in HBM.
 //   logits      m vocabulary (W, k along rows)    n tokens (x, k along rows)
 //   d^T[v][t]   m tokens (x, k along rows)        n vocabulary (W, k along rows)
@@ -56,17 +56,17 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
   int pm, pn;
   tile_place(blockIdx.x, (V + TILE - 1) / TILE, (T + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
-  floatx16 acc[4][2];
+  floatx16 acc[4][4];
   tile_product<false, false>(TileOperand{w + (int64_t)m0 * ld_w, ld_w, V - m0, H},
                              TileOperand{x + (int64_t)n0 * ld_x, ld_x, T - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
   const int rows = V - m0 - wm * 128 - 4 * h;  // vocabulary rows from the lane's first
-  float2 st[2];
+  float2 st[4];
 #pragma unroll
-  for (int j = 0; j < 2; j++) {
-    const int t = n0 + wn * 64 + 32 * j + lr;
+  for (int j = 0; j < 4; j++) {
+    const int t = n0 + wn * 128 + 32 * j + lr;
     if (V - m0 < TILE) {
 #pragma unroll
       for (int i = 0; i < 4; i++)
@@ -78,11 +78,16 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
     const int64_t label = t < T ? labels[t] : -1;
     const int lab = label >= 0 && label < V ? (int)label - m0 - wm * 128 - 4 * h : -1;
     if (__any(lab >= 0 && lab < 128)) {
+      float z = 0.0f;
+      bool mine = false;  // rows alternate in fours between the lanes of a column
 #pragma unroll
       for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int r = 0; r < 16; r++)
-          if (lab == tile_row(i, r)) zlab[t] = acc[i][j][r];
+        for (int r = 0; r < 16; r++) {
+          z = lab == tile_row(i, r) ? acc[i][j][r] : z;
+          mine = mine || lab == tile_row(i, r);
+        }
+      if (mine) zlab[t] = z;
     }
     float mx = -INFINITY;
 #pragma unroll
@@ -103,12 +108,12 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
   __syncthreads();
   float2* half = reinterpret_cast<float2*>(lds);
   if (wm == 1 && h == 0)
-    for (int j = 0; j < 2; j++) half[wn * 64 + 32 * j + lr] = st[j];
+    for (int j = 0; j < 4; j++) half[wn * 128 + 32 * j + lr] = st[j];
   __syncthreads();
   if (wm == 0 && h == 0)
-    for (int j = 0; j < 2; j++) {
-      const int t = n0 + wn * 64 + 32 * j + lr;
-      if (t < T) stats[(int64_t)pm * T + t] = join(st[j], half[wn * 64 + 32 * j + lr]);
+    for (int j = 0; j < 4; j++) {
+      const int t = n0 + wn * 128 + 32 * j + lr;
+      if (t < T) stats[(int64_t)pm * T + t] = join(st[j], half[wn * 128 + 32 * j + lr]);
     }
 }
 
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
   tile_place(blockIdx.x, tiles_t, (rows + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
   if (m0 >= n_tok) return;
-  floatx16 acc[4][2];
+  floatx16 acc[4][4];
   tile_product<false, false>(TileOperand{xc + (int64_t)m0 * H, (uint32_t)H, n_tok - m0, H},
                              TileOperand{w + (int64_t)n0 * ld_w, ld_w, rows - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
@@ -228,32 +233,40 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
   }
   __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
-  // a label of the wave's 128 tokens among its 64 vocabulary rows?
-  const int lab0 = s_lab[wm * 128 + lane] >> 6, lab1 = s_lab[wm * 128 + 64 + lane] >> 6;  // -1 stays -1
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
+  // a label of the wave's 128 tokens among its 128 vocabulary rows?
+  const int lab0 = s_lab[wm * 128 + lane] >> 7, lab1 = s_lab[wm * 128 + 64 + lane] >> 7;  // -1 stays -1
   const bool hit = __any(lab0 == wn || lab1 == wn);
+  auto put = [&](auto with_labels) {
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+    for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int m = wm * 128 + 32 * i + 8 * q + 4 * h;
-      const float4 l = *reinterpret_cast<const float4*>(s_lse + m);
-      const float4 g = *reinterpret_cast<const float4*>(s_g + m);
-      const int4 lab = *reinterpret_cast<const int4*>(s_lab + m);
+      for (int q = 0; q < 4; q++) {
+        const int m = wm * 128 + 32 * i + 8 * q + 4 * h;
+        const float4 l = *reinterpret_cast<const float4*>(s_lse + m);
+        const float4 g = *reinterpret_cast<const float4*>(s_g + m);
+        int4 lab = make_int4(-1, -1, -1, -1);
+        if constexpr (with_labels.value) lab = *reinterpret_cast<const int4*>(s_lab + m);
 #pragma unroll
-      for (int j = 0; j < 2; j++) {
-        const int n = wn * 64 + 32 * j + lr;
-        float p0 = exp_fast(acc[i][j][4 * q] - l.x), p1 = exp_fast(acc[i][j][4 * q + 1] - l.y);
-        float p2 = exp_fast(acc[i][j][4 * q + 2] - l.z), p3 = exp_fast(acc[i][j][4 * q + 3] - l.w);
-        if (hit) {
-          p0 -= lab.x == n ? 1.0f : 0.0f;
-          p1 -= lab.y == n ? 1.0f : 0.0f;
-          p2 -= lab.z == n ? 1.0f : 0.0f;
-          p3 -= lab.w == n ? 1.0f : 0.0f;
+        for (int j = 0; j < 4; j++) {
+          const int n = wn * 128 + 32 * j + lr;
+          float p0 = exp_fast(acc[i][j][4 * q] - l.x), p1 = exp_fast(acc[i][j][4 * q + 1] - l.y);
+          float p2 = exp_fast(acc[i][j][4 * q + 2] - l.z), p3 = exp_fast(acc[i][j][4 * q + 3] - l.w);
+          if constexpr (with_labels.value) {
+            p0 -= lab.x == n ? 1.0f : 0.0f;
+            p1 -= lab.y == n ? 1.0f : 0.0f;
+            p2 -= lab.z == n ? 1.0f : 0.0f;
+            p3 -= lab.w == n ? 1.0f : 0.0f;
+          }
+          tile_put(lds, n, m >> 3, h, bf16_pack(p0 * g.x, p1 * g.y), bf16_pack(p2 * g.z, p3 * g.w));
         }
-        tile_put(lds, n, m >> 3, h, bf16_pack(p0 * g.x, p1 * g.y), bf16_pack(p2 * g.z, p3 * g.w));
+        __builtin_amdgcn_sched_barrier(0);  // few token values at a time beside 256 accumulators
       }
-    }
+  };
+  if (hit)
+    put(std::true_type{});
+  else
+    put(std::false_type{});
   __syncthreads();
   const int padded = (rows + 63) / 64 * 64;
   for (int e = threadIdx.x; e < TILE * 32; e += TILE_THREADS) {
@@ -283,7 +296,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dw(const uint16_t* xc, int 
   tile_place(blockIdx.x, (H + TILE - 1) / TILE, (rows + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
   const int K = (n_tok + 63) / 64 * 64;
-  floatx16 acc[4][2];
+  floatx16 acc[4][4];
   if (K > 0) {
     tile_product<true, false>(TileOperand{xc + m0, (uint32_t)H, H - m0, K},
                               TileOperand{d + (int64_t)n0 * ldd, (uint32_t)ldd, rows - n0, K}, K, 0, K / TILE_K, lds, acc);
@@ -291,20 +304,20 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dw(const uint16_t* xc, int 
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
-      for (int j = 0; j < 2; j++)
+      for (int j = 0; j < 4; j++)
 #pragma unroll
         for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
   }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 2; j++)
+  for (int j = 0; j < 4; j++)
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int m = wm * 128 + 32 * i + 8 * q + 4 * h, n = wn * 64 + 32 * j + lr;
+        const int m = wm * 128 + 32 * i + 8 * q + 4 * h, n = wn * 128 + 32 * j + lr;
         const bool in = n0 + n < rows && m0 + m < H;  // H is a multiple of 8
         OutT* out = dw + (int64_t)(n0 + n) * ld_dw + m0 + m;
         float v[4];
@@ -358,26 +371,26 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dx_sum(const uint16_t* w, u
   if (kt0 == kt1) {  // fewer stages than parts: nothing to add
     if (accumulate) return;
   }
-  floatx16 acc[4][2];
+  floatx16 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int j = 0; j < 2; j++)
+    for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
   if (kt0 < kt1)
     tile_product<true, true>(TileOperand{w + m0, ld_w, H - m0, rows},
                              TileOperand{d + n0, (uint32_t)ldd, (int)(ldd - n0), KT * TILE_K}, rows, kt0, kt1, lds, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = wave >> 2, wn = wave & 3, h = lane >> 5, lr = lane & 31;
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
   float* out = sum + (int64_t)part * T * H;
 #pragma unroll
-  for (int j = 0; j < 2; j++)
+  for (int j = 0; j < 4; j++)
 #pragma unroll
     for (int i = 0; i < 4; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int m = m0 + wm * 128 + 32 * i + 8 * q + 4 * h, n = n0 + wn * 64 + 32 * j + lr;
+        const int m = m0 + wm * 128 + 32 * i + 8 * q + 4 * h, n = n0 + wn * 128 + 32 * j + lr;
         if (n >= n_tok || m >= H) continue;
         float4* o = reinterpret_cast<float4*>(out + (int64_t)n * H + m);
         float4 s = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
