@@ -38,13 +38,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "layers_device.hpp"
+#include "loss_device.hpp"
 
 namespace nvfp4 {
 
 namespace {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(1))) void tile_gvoid;
 typedef __attribute__((address_space(3))) void tile_lvoid;

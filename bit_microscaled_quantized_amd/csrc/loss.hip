@@ -18,8 +18,8 @@
 //   dW[v][h]    m hidden (x, k down columns)      n vocabulary (d^T, k along rows)
 //   dx[t][h]    m hidden (W, k down columns)      n tokens (d^T, k down columns)
 #include "bf16_tile.hpp"
-#include "layers_device.hpp"
 #include "layers_launch.hpp"
+#include "loss_device.hpp"
 
 #include <mutex>
 
@@ -27,27 +27,10 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// exp(a): one multiply and the hardware's 2^x, within 1 ulp of exp(a (1 + 2^-24));
-// results below 2^-126 are 0.
-__device__ __forceinline__ float exp_fast(float a) { return __builtin_amdgcn_exp2f(a * kLog2e); }
-
-// (maximum m, sum of exp(z - m)) of some of a token's logits.  An infinite
-// maximum (no logits, only -inf among them, or a +inf) is taken as 0 in the
-// exponents, so that the sum is 0, inf or NaN as it is without the shift.
-__device__ __forceinline__ float shift_of(float m) { return __builtin_fabsf(m) == INFINITY ? 0.0f : m; }
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x);
-  const float fa = __builtin_fabsf(a.x) == INFINITY ? 1.0f : expf(a.x - m);
-  const float fb = __builtin_fabsf(b.x) == INFINITY ? 1.0f : expf(b.x - m);
-  return make_float2(m, a.y * fa + b.y * fb);
-}
-
 // Row m of the tile of register r of MFMA tile i, without the lane's 4 h.
 __device__ __forceinline__ int tile_row(int i, int r) { return 32 * i + 8 * (r >> 2) + (r & 3); }
 
-// stats[vt][t] = the pair of vocabulary tile vt and token t; zlab[t] = the
+// stats[t][vt] = the pair of token t and vocabulary tile vt; zlab[t] = the
 // logit of t's label.
 __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
                                                                   const uint16_t* x, uint32_t ld_x, int T, int H,
@@ -113,24 +96,24 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
   if (wm == 0 && h == 0)
     for (int j = 0; j < 4; j++) {
       const int t = n0 + wn * 128 + 32 * j + lr;
-      if (t < T) stats[(int64_t)pm * T + t] = join(st[j], half[wn * 128 + 32 * j + lr]);
+      if (t < T) stats[(int64_t)t * ((V + TILE - 1) / TILE) + pm] = join(st[j], half[wn * 128 + 32 * j + lr]);
     }
 }
 
-// lse and loss of a token from its `tiles` pairs: 64 tokens per workgroup,
-// four slices of tiles each.
-__global__ __launch_bounds__(256) void k_loss(const float2* stats, int tiles, int64_t T, int64_t V,
-                                              const int64_t* labels, const float* zlab, float* loss, float* lse) {
-  __shared__ float2 part[4][64];
-  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 64 + lane;
+// lse and loss of a token from its `tiles` pairs: one workgroup per token.
+__global__ __launch_bounds__(256) void k_loss(const float2* stats, int tiles, int V, const int64_t* labels,
+                                              const float* zlab, float* loss, float* lse) {
+  __shared__ float2 part[4];
+  const int64_t t = blockIdx.x;
   float2 st = make_float2(-INFINITY, 0.0f);
-  if (t < T)
-    for (int q = tiles * slice / 4; q < tiles * (slice + 1) / 4; q++) st = join(st, stats[(int64_t)q * T + t]);
-  part[slice][lane] = st;
+  for (int q = threadIdx.x; q < tiles; q += 256) st = join(st, stats[t * tiles + q]);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) st = join(st, make_float2(__shfl_xor(st.x, m, 64), __shfl_xor(st.y, m, 64)));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = st;
   __syncthreads();
-  if (slice != 0 || t >= T) return;
-  for (int q = 1; q < 4; q++) st = join(st, part[q][lane]);
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int q = 1; q < 4; q++) st = join(st, part[q]);
   const float l = st.x + logf(st.y);
   lse[t] = l;
   const int64_t lab = labels[t];
@@ -138,14 +121,6 @@ __global__ __launch_bounds__(256) void k_loss(const float2* stats, int tiles, in
 }
 
 // ---- backward: the tokens that have a label come first
-
-// What the backward pass knows of its n[0] labelled tokens, in order: their
-// labels, lse, dloss, and of every token its place among them (or -1).
-struct Tokens {
-  int* n;
-  int* place;
-  int* list;
-};
 
 // One workgroup: token t's place is the number of labelled tokens before it.
 __global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, int64_t T, int64_t V, Tokens tk) {
@@ -459,20 +434,31 @@ int64_t dx_parts(int64_t T, int64_t H, int64_t piece) {
 // The backward workspace: offsets of its parts.
 struct BackPlan {
   int64_t piece, ldd, parts;
-  int64_t d, xc, sum, tok, end;
+  int64_t dt, d, xc, sum, tok, end;
 };
 BackPlan back_plan(int64_t T, int64_t V, int64_t H) {
   BackPlan p;
-  p.piece = piece_rows(T, V);
-  p.ldd = up64(T);
-  p.parts = dx_parts(T, H, p.piece);
-  p.d = 0;
-  p.xc = p.d + up16(up64(p.piece) * p.ldd * 2);
+  p.dt = 0;
+  if (T <= FEW_TOKENS) {  // the whole vocabulary at once, d in both orientations
+    p.piece = V;
+    p.ldd = few_ldt(T);
+    p.parts = few_dx_parts(T, V, H);
+    p.d = up16(few_rows(V) * p.ldd * 2);
+    p.xc = p.d + up16(few_tokens(T) * few_rows(V) * 2);
+  } else {
+    p.piece = piece_rows(T, V);
+    p.ldd = up64(T);
+    p.parts = dx_parts(T, H, p.piece);
+    p.d = p.xc = up16(up64(p.piece) * p.ldd * 2);
+  }
   p.sum = p.xc + up16(up64(T) * H * 2);
   p.tok = p.sum + up16(p.parts * T * H * 4);
   p.end = p.tok + up16((2 * T + 1) * 4);
   return p;
 }
+
+// Vocabulary tiles of the forward's pairs.
+int64_t stats_tiles(int64_t T, int64_t V) { return T <= FEW_TOKENS ? few_rows(V) / FEW_ROWS : tiles_of(V); }
 
 // Largest dynamic LDS of every tile kernel, set once.
 constexpr int kTileLds = TILE_LDS + 3 * TILE * 4;
@@ -492,23 +478,29 @@ hipError_t allow_lds() {
 }  // namespace
 
 int64_t linear_ce_workspace(int64_t T, int64_t V, int64_t H, bool train) {
-  const int64_t fwd = up16(tiles_of(V) * T * 8) + up16(T * 4);
+  const int64_t fwd = up16(stats_tiles(T, V) * T * 8) + up16(T * 4);
   return train ? std::max(fwd, back_plan(T, V, H).end) : fwd;
 }
 
 hipError_t launch_linear_ce(int64_t T, int64_t V, int64_t H, const void* x, int64_t ld_x, const void* w, int64_t ld_w,
                             const int64_t* labels, float* loss, float* lse, void* workspace, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  hipError_t e = allow_lds();
-  if (e != hipSuccess) return e;
-  const int tiles = (int)tiles_of(V);
+  const int tiles = (int)stats_tiles(T, V);
   float2* stats = static_cast<float2*>(workspace);
   float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16((int64_t)tiles * T * 8));
-  k_logits_stats<<<(unsigned)(tiles * tiles_of(T)), TILE_THREADS, kTileLds, s>>>(
-      static_cast<const uint16_t*>(w), (uint32_t)ld_w, (int)V, static_cast<const uint16_t*>(x), (uint32_t)ld_x, (int)T,
-      (int)H, labels, stats, zlab);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  k_loss<<<(unsigned)((T + 63) / 64), 256, 0, s>>>(stats, tiles, T, V, labels, zlab, loss, lse);
+  const uint16_t* wp = static_cast<const uint16_t*>(w);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  hipError_t e;
+  if (T <= FEW_TOKENS) {
+    e = few_stats(wp, (uint32_t)ld_w, V, xp, (uint32_t)ld_x, T, H, labels, stats, zlab, s);
+  } else {
+    if ((e = allow_lds()) != hipSuccess) return e;
+    k_logits_stats<<<(unsigned)(tiles * tiles_of(T)), TILE_THREADS, kTileLds, s>>>(
+        wp, (uint32_t)ld_w, (int)V, xp, (uint32_t)ld_x, (int)T, (int)H, labels, stats, zlab);
+    e = hipGetLastError();
+  }
+  if (e != hipSuccess) return e;
+  k_loss<<<(unsigned)T, 256, 0, s>>>(stats, tiles, (int)V, labels, zlab, loss, lse);
   return hipGetLastError();
 }
 
@@ -522,19 +514,31 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     k_zero<<<(unsigned)V, 256, 0, s>>>(dw, H * es, ld_dw * es);
     return hipGetLastError();
   }
-  hipError_t e = allow_lds();
-  if (e != hipSuccess) return e;
   const BackPlan pl = back_plan(T, V, H);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.d);
+  uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.dt);  // d^T
   uint16_t* xc = reinterpret_cast<uint16_t*>(ws + pl.xc);
   float* sum = reinterpret_cast<float*>(ws + pl.sum);
   int* tok = reinterpret_cast<int*>(ws + pl.tok);
   const Tokens tk{tok, tok + 1, tok + 1 + T};
   k_tokens<<<1, 1024, 0, s>>>(labels, T, V, tk);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   k_gather<<<(unsigned)up64(T), 256, 0, s>>>(static_cast<const uint16_t*>(x), ld_x, H, tk, xc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (T <= FEW_TOKENS) {
+    uint16_t* dr = reinterpret_cast<uint16_t*>(ws + pl.d);
+    const uint16_t* wp = static_cast<const uint16_t*>(w);
+    e = few_grad(wp, (uint32_t)ld_w, V, xc, T, H, tk, labels, lse, dloss, d, dr, s);
+    if (e == hipSuccess && dw != nullptr)
+      e = few_dw(xc, H, d, pl.ldd, V, T, tk, dw, dw_dt, ld_dw, accumulate, s);
+    if (e == hipSuccess && dx != nullptr) e = few_dx(wp, (uint32_t)ld_w, V, dr, T, H, tk, sum, s);
+    if (e != hipSuccess) return e;
+    if (dx != nullptr)
+      k_dx<<<(unsigned)T, 256, 0, s>>>(sum, (int)pl.parts, T, H, tk, static_cast<uint16_t*>(dx), ld_dx);
+    return hipGetLastError();
+  }
+  if ((e = allow_lds()) != hipSuccess) return e;
   const int tt = (int)tiles_of(T);
   const int64_t th = tiles_of(H);
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
@@ -544,7 +548,10 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     k_logits_grad<<<(unsigned)(tt * tv), TILE_THREADS, kTileLds, s>>>(wp, (uint32_t)ld_w, (int)n, xc, (int)H, tt, v0,
                                                                       tk, labels, lse, dloss, d, pl.ldd);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (dw != nullptr) {
+    if (dw != nullptr && T <= FEW_DW_TOKENS) {
+      void* out = static_cast<uint8_t*>(dw) + v0 * ld_dw * (dw_dt == 0 ? 2 : 4);
+      if ((e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, s)) != hipSuccess) return e;
+    } else if (dw != nullptr) {
       if (dw_dt == 0)
         k_dw<<<(unsigned)(th * tv), TILE_THREADS, kTileLds, s>>>(
             xc, (int)H, d, pl.ldd, (int)n, tk, static_cast<uint16_t*>(dw) + v0 * ld_dw, ld_dw, accumulate);
