@@ -1,26 +1,30 @@
-// One 256 x 256 tile of a BF16 matrix product with FP32 accumulation on gfx950:
+// One tile of a BF16 matrix product with FP32 accumulation on gfx950, 256 x 256
+// (W = 4) or 128 x 128 (W = 2):
 //   acc(m, n) = sum_k A(m, k) B(n, k)
 // for operands that hold K along their rows (element (m, k) at p[m * ld + k]) or
 // down their columns (KMAJOR, element (m, k) at p[k * ld + m]).
 //
-// 256 threads = 4 waves, one per SIMD, in a 2 x 2 grid; wave tile 128 x 128 =
-// 4 x 4 MFMA tiles of 32 x 32 x 16 (256 FP32 accumulators a lane).  The chip's
+// 256 threads = 4 waves, one per SIMD, in a 2 x 2 grid; wave tile of W x W MFMA
+// tiles of 32 x 32 x 16 (W = 4: 256 FP32 accumulators a lane).  The chip's
 // power limits this product, not its matrix rate (at full occupation of the
 // matrix cores by random data the clock falls from 2.4 to 1.8 GHz), so what
 // counts is energy per product: the square wave tile reads a third less from LDS
 // than 8 waves of 128 x 64 (32768 x 8192 x 5120: 1.98 ms against 2.20, 1386
 // against 1250 TFLOP/s).  A stage is 64 values of k: 32 KB per operand, fetched
-// straight into LDS (two buffers, 128 KB), 16 bytes per lane in whole 128-byte
+// straight into LDS (two buffers, 128 KB; W = 2: half), 16 bytes per lane in whole 128-byte
 // lines (stages of 32 values, twice as many in flight, run their 64-byte requests
 // at more energy: 2.25 ms).  With one wave per SIMD nothing else hides a wait, so
 // the reads and fetches are placed between the matrix instructions by hand.
+// The small tile fits twice on a compute unit, so that one workgroup's start and
+// end overlap the other's products: it is for products with few large tiles or
+// few stages.
 //
 // LDS layouts, both free of bank conflicts (64 banks of 4 bytes):
-//   * K along rows: 256 rows of 128 bytes; the 16-byte chunk c of row r lies in
+//   * K along rows: rows of 128 bytes; the 16-byte chunk c of row r lies in
 //     slot 8 r + (c ^ ((r >> 1) & 7)).  A fragment (row lr, 8 values of k) is one
 //     16-byte read.
-//   * KMAJOR: 64 rows (k) of 512 bytes; the 16-byte chunk g of row k lies in slot
-//     32 k + (g ^ ((k & 3) << 2)).  A fragment is two transposing 8-byte reads
+//   * KMAJOR: 64 rows (k) of 8 W chunks of 16 bytes; chunk g of row k lies in slot
+//     8 W k + (g ^ ((k & 3) << 2)).  A fragment is two transposing 8-byte reads
 //     (ds_read_b64_tr_b16): in a block of 16 lanes, lane i names 4 values of m,
 //     4 (i & 3) .., in row i >> 2, and receives those 4 rows' values at m = i.
 //
@@ -29,10 +33,9 @@
 // (r & 3), r = 0 .. 15.
 //
 // Addresses stay inside the operands: rows of a tile past the last are fetched
-// from the last row (or, KMAJOR, from the last 8 columns) and never used.  Where
-// K is not a multiple of 64 (it is one of 8), an operand with K along its rows
-// gets zeros past K from the last stage; a KMAJOR operand is read up to its own
-// last row of k, and one of the two must give zeros past K.
+// from the last row (or, KMAJOR, from the last 8 columns) and never used, and a
+// KMAJOR operand's values of k past its last from that one.  K along rows may end
+// inside a stage (K a multiple of 8): zeros follow it.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -49,12 +52,11 @@ typedef __attribute__((address_space(1))) void tile_gvoid;
 typedef __attribute__((address_space(3))) void tile_lvoid;
 typedef __attribute__((address_space(3))) s16x4_t tile_ls16x4;
 
-constexpr int TILE = 256;               // both ways
-constexpr int TILE_K = 64;              // values of k per stage
-constexpr int TILE_OPERAND = 32 * 1024;  // bytes of an operand's stage
-constexpr int TILE_STAGE = 2 * TILE_OPERAND;
-constexpr int TILE_LDS = 2 * TILE_STAGE;
+constexpr int TILE_K = 64;  // values of k per stage
 constexpr int TILE_THREADS = 256;
+constexpr int tile_side(int W) { return 64 * W; }
+constexpr int tile_operand(int W) { return tile_side(W) * TILE_K * 2; }  // bytes of an operand's stage
+constexpr int tile_lds(int W) { return 4 * tile_operand(W); }            // two buffers of both operands
 
 // An operand of a tile: its first element (m = the tile's first row, k = 0),
 // leading dimension, and rows from there on (at least one; KMAJOR: rounded up to
@@ -67,62 +69,63 @@ struct TileOperand {
   int krows;
 };
 
-// Fetch offsets (bytes) of a lane's eight 16-byte loads of a stage: load j of a
-// wave fills bytes 1024 (8 wave + j) .. of the operand's stage.
-template <bool KMAJOR>
+// Fetch offsets (bytes) of a lane's 2 W 16-byte loads of a stage: load j of a wave
+// fills bytes 1024 (2 W wave + j) .. of the operand's stage.
+template <int W, bool KMAJOR>
 struct TileFetch {
-  uint32_t off[8];
-  __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane, int krows) {
+  uint32_t off[2 * W];
+  static __device__ __forceinline__ int row(int wave, int lane, int j) {  // K along rows
+    return 8 * (2 * W * wave + j) + (lane >> 3);
+  }
+  static __device__ __forceinline__ int krow(int wave, int lane, int j) {  // KMAJOR
+    return ((2 * W * wave + j) * 64 + lane) / (8 * W);
+  }
+  // K along rows: the whole offset; KMAJOR: that of the columns
+  __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
+    for (int j = 0; j < 2 * W; j++) {
       if constexpr (!KMAJOR) {
-        const int r = 8 * (8 * wave + j) + (lane >> 3);
+        const int r = row(wave, lane, j);
         off[j] = (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
       } else {
-        const int k = 2 * (8 * wave + j) + (lane >> 5);
-        const int g = (lane & 31) ^ ((k & 3) << 2);
-        off[j] = (uint32_t)min(k, krows - 1) * (o.ld * 2) + 2 * min(8 * g, o.rows - 8);
+        const int g = ((j * 64 + lane) % (8 * W)) ^ ((krow(wave, lane, j) & 3) << 2);
+        off[j] = 2 * min(8 * g, o.rows - 8);
       }
     }
   }
   // load j of stage kt
-  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int j) const {
+  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int lane, int j) const {
+    if constexpr (KMAJOR) kt = min(kt, (o.krows - 1) / TILE_K);
     const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
                           (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
     uint32_t v = off[j];
+    if constexpr (KMAJOR) v += (uint32_t)min(krow(wave, lane, j), o.krows - 1 - kt * TILE_K) * (o.ld * 2);
     asm volatile("" : "+v"(v));  // a 32-bit offset register beside the scalar base
-    __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (8 * wave + j) * 1024), 16, 0, 0);
+    __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (2 * W * wave + j) * 1024), 16, 0, 0);
   }
 };
 
-// The last stage, K not a multiple of 64: zeros past K (K along rows), or rows up
-// to the operand's last (KMAJOR).
-template <bool KMAJOR>
+// The last stage of an operand with K along its rows, K not a multiple of 64.
+template <int W>
 __device__ __forceinline__ void tile_last(const TileOperand& o, int kt, int K, uint8_t* st, int wave, int lane) {
-  if constexpr (KMAJOR) {
-    TileFetch<true> f;
-    f.init(o, wave, lane, o.krows - kt * TILE_K);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) + (int64_t)kt * TILE_K * 2;
 #pragma unroll
-    for (int j = 0; j < 8; j++) f.issue(o, kt, st, wave, j);
-  } else {
-    const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) + (int64_t)kt * TILE_K * 2;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const int r = 8 * (8 * wave + j) + (lane >> 3);
-      const int c = (lane & 7) ^ ((r >> 1) & 7);
-      u32x4_t v = {0, 0, 0, 0};
-      if (kt * TILE_K + 8 * c < K)
-        v = *reinterpret_cast<const u32x4_t*>(base + (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * c);
-      *reinterpret_cast<u32x4_t*>(st + (8 * wave + j) * 1024 + lane * 16) = v;
-    }
+  for (int j = 0; j < 2 * W; j++) {
+    const int r = TileFetch<W, false>::row(wave, lane, j);
+    const int c = (lane & 7) ^ ((r >> 1) & 7);
+    u32x4_t v = {0, 0, 0, 0};
+    if (kt * TILE_K + 8 * c < K)
+      v = *reinterpret_cast<const u32x4_t*>(base + (uint32_t)min(r, o.rows - 1) * (o.ld * 2) + 16 * c);
+    *reinterpret_cast<u32x4_t*>(st + (2 * W * wave + j) * 1024 + lane * 16) = v;
   }
 }
 
-// Fragments of the wave's four MFMA tiles from row `first` of the operand's stage.
-template <bool KMAJOR>
+// Fragments of the wave's W MFMA tiles from row `first` of the operand's stage.
+template <int W, bool KMAJOR>
 struct TileFrag {
-  uint32_t at[KMAJOR ? 4 : 1];
+  uint32_t at[KMAJOR ? W : 1];
   uint32_t x;
+  static constexpr int ROW = 128 * W;  // bytes of a row of k (KMAJOR)
   __device__ __forceinline__ void init(int first, int lane) {
     if constexpr (!KMAJOR) {
       at[0] = (uint32_t)(first + (lane & 31)) * 128;
@@ -131,9 +134,9 @@ struct TileFrag {
       const int b = lane >> 4, i = lane & 15;
       x = 0;
 #pragma unroll
-      for (int t = 0; t < 4; t++) {
+      for (int t = 0; t < W; t++) {
         const int g = (((first >> 3) + 4 * t) ^ ((i >> 2) << 2)) + 2 * (b & 1) + ((i & 3) >> 1);
-        at[t] = (uint32_t)(8 * (b >> 1) + (i >> 2)) * 512 + g * 16 + (i & 1) * 8;
+        at[t] = (uint32_t)(8 * (b >> 1) + (i >> 2)) * ROW + g * 16 + (i & 1) * 8;
       }
     }
   }
@@ -141,129 +144,141 @@ struct TileFrag {
     if constexpr (!KMAJOR) {
       return *reinterpret_cast<const bf16x8_t*>(st + at[0] + t * 32 * 128 + (((2 * s + h) ^ x) << 4));
     } else {
-      const uint8_t* p = st + at[t] + s * 16 * 512;
+      const uint8_t* p = st + at[t] + s * 16 * ROW;
       const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_ls16x4*)(p));
-      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_ls16x4*)(p + 4 * 512));
+      const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_ls16x4*)(p + 4 * ROW));
       return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   }
 };
 
-// acc = the product over the stages kt0 .. kt1 - 1 of K values of k.  All waves
-// of the workgroup take part; the caller's LDS stages are free again after its
-// next barrier.
-template <bool AMAJ, bool BMAJ>
+// acc = the product over the stages kt0 .. kt1 - 1 of K values of k.  EVEN: their
+// number is even and K a multiple of 64 (the caller's operands hold zeros up to
+// there); without it both operands have K along their rows.  All waves of the
+// workgroup take part; the caller's LDS stages are free again after its next
+// barrier.
+template <int W, bool AMAJ, bool BMAJ, bool EVEN>
 __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOperand& b, int K, int kt0, int kt1,
-                                             uint8_t* lds, floatx16 (&acc)[4][4]) {
+                                             uint8_t* lds, floatx16 (&acc)[W][W]) {
+  constexpr int OPERAND = tile_operand(W), STAGE = 2 * OPERAND;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5;
-  TileFetch<AMAJ> fa;
-  TileFetch<BMAJ> fb;
-  fa.init(a, wave, lane, TILE_K);
-  fb.init(b, wave, lane, TILE_K);
-  TileFrag<AMAJ> ra;
-  TileFrag<BMAJ> rb;
-  ra.init((wave >> 1) * 128, lane);
-  rb.init((wave & 1) * 128, lane);
+  TileFetch<W, AMAJ> fa;
+  TileFetch<W, BMAJ> fb;
+  static_assert(EVEN || (!AMAJ && !BMAJ), "odd stages are for K along rows");
+  fa.init(a, wave, lane);
+  fb.init(b, wave, lane);
+  TileFrag<W, AMAJ> ra;
+  TileFrag<W, BMAJ> rb;
+  ra.init((wave >> 1) * 32 * W, lane);
+  rb.init((wave & 1) * 32 * W, lane);
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+  for (int i = 0; i < W; i++)
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int j = 0; j < W; j++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-  bf16x8_t va[2][4], vb[2][4];
+  bf16x8_t va[2][W], vb[2][W];
 
   // The stage that ends past K, and one more where the rest is odd, go first,
   // each fetched and multiplied by itself.
-  auto alone = [&](int kt, bool ragged) {
-    if (ragged) {
-      tile_last<AMAJ>(a, kt, K, lds, wave, lane);
-      tile_last<BMAJ>(b, kt, K, lds + TILE_OPERAND, wave, lane);
-    } else {
+  int first = kt0, end = kt1;
+  if constexpr (!EVEN) {
+    auto alone = [&](int kt, bool ragged) {
+      if (ragged) {
+        tile_last<W>(a, kt, K, lds, wave, lane);
+        tile_last<W>(b, kt, K, lds + OPERAND, wave, lane);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        fa.issue(a, kt, lds, wave, j);
-        fb.issue(b, kt, lds + TILE_OPERAND, wave, j);
+        for (int j = 0; j < 2 * W; j++) {
+          fa.issue(a, kt, lds, wave, lane, j);
+          fb.issue(b, kt, lds + OPERAND, wave, lane, j);
+        }
       }
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
 #pragma unroll 1
-    for (int s = 0; s < 4; s++) {
+      for (int s = 0; s < 4; s++) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        va[0][i] = ra.read(lds, i, s, h);
-        vb[0][i] = rb.read(lds + TILE_OPERAND, i, s, h);
+        for (int i = 0; i < W; i++) {
+          va[0][i] = ra.read(lds, i, s, h);
+          vb[0][i] = rb.read(lds + OPERAND, i, s, h);
+        }
+#pragma unroll
+        for (int i = 0; i < W; i++)
+#pragma unroll
+          for (int j = 0; j < W; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[0][i], vb[0][j], acc[i][j], 0, 0, 0);
       }
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[0][i], vb[0][j], acc[i][j], 0, 0, 0);
-    }
-    __syncthreads();
-  };
-  bool ragged = (K & (TILE_K - 1)) != 0 && kt1 * TILE_K > K;
-  int first = kt0, end = ragged ? kt1 - 1 : kt1;
-  const bool odd = ((end - first) & 1) != 0;
-  if (ragged || odd) {
+      __syncthreads();
+    };
+    const bool ragged = (K & (TILE_K - 1)) != 0 && kt1 * TILE_K > K;
+    if (ragged) end--;
+    const bool odd = ((end - first) & 1) != 0;
+    if (ragged || odd) {
 #pragma unroll 1
-    for (int pass = 0; pass < 2; pass++) {
-      if (pass == 0 ? ragged : odd) alone(pass == 0 ? end : first, pass == 0);
+      for (int pass = 0; pass < 2; pass++) {
+        if (pass == 0 ? ragged : odd) alone(pass == 0 ? end : first, pass == 0);
+      }
+      if (odd) first++;
     }
-    if (odd) first++;
+    if (first == end) return;
   }
-  if (first == end) return;
 
-  // A stage is four steps of 16 values of k, 16 matrix instructions each.  Each
+  // A stage is four steps of 16 values of k, W x W matrix instructions each.  Each
   // step first reads the next step's fragments, two reads after each of its first
-  // four matrix instructions (of the next stage, after the barrier that ends a
-  // stage, in the last step).  A stage's loads are issued between the matrix
-  // instructions of two steps: half of them as soon as their buffer is free,
-  // after that barrier, half in the step after.  (All at once they keep the wave
-  // from the matrix core until the address unit has taken them; later, they have
-  // not landed when the stage ends.)  The last two stages' loads are clamped to
-  // the last stage, so that every stage is the same code; what they fetch is not
-  // read.  The schedule barriers hold the order as written.
+  // W matrix instructions (of the next stage, after the barrier that ends a stage,
+  // in the last step).  A stage's loads are issued between the matrix instructions
+  // of two steps: half of them as soon as their buffer is free, after that barrier,
+  // half in the step after.  (All at once they keep the wave from the matrix core
+  // until the address unit has taken them; later, they have not landed when the
+  // stage ends.)  The last two stages' loads are clamped to the last stage, so that
+  // every stage is the same code; what they fetch is not read.  The schedule
+  // barriers hold the order as written.
 #define TILE_FENCE __builtin_amdgcn_sched_barrier(0)
-#define TILE_READ(st, s, q, x)                                     \
-  do {                                                             \
-    if ((x) == 0)                                                  \
-      va[q][0] = ra.read(st, 0, s, h);                             \
-    else if ((x) < 5)                                              \
-      vb[q][(x)-1] = rb.read((st) + TILE_OPERAND, (x)-1, s, h);    \
-    else                                                           \
-      va[q][(x)-4] = ra.read(st, (x)-4, s, h);                     \
+#define TILE_READ(st, s, q, x)                                 \
+  do {                                                         \
+    if ((x) == 0)                                              \
+      va[q][0] = ra.read(st, 0, s, h);                         \
+    else if ((x) <= W)                                         \
+      vb[q][((x) - 1) % W] = rb.read((st) + OPERAND, ((x) - 1) % W, s, h); \
+    else                                                       \
+      va[q][(x) - W] = ra.read(st, (x) - W, s, h);             \
   } while (0)
-#define TILE_LOAD(kt, st, x)                              \
-  do {                                                    \
-    if ((x)&1)                                            \
-      fb.issue(b, kt, (st) + TILE_OPERAND, wave, (x) >> 1); \
-    else                                                  \
-      fa.issue(a, kt, st, wave, (x) >> 1);                \
+#define TILE_LOAD(kt, st, x)                             \
+  do {                                                   \
+    if ((x) & 1)                                         \
+      fb.issue(b, kt, (st) + OPERAND, wave, lane, (x) >> 1);   \
+    else                                                 \
+      fa.issue(a, kt, st, wave, lane, (x) >> 1);               \
   } while (0)
-  // fragments q in use; the next step's from step rs of rst; loads x0 .. x0 + 7 of stage kt into dst
-#define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                       \
-  do {                                                                                                  \
-    _Pragma("unroll") for (int m = 0; m < 16; m++) {                                                    \
-      acc[m >> 2][m & 3] =                                                                              \
-          __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q][m >> 2], vb[q][m & 3], acc[m >> 2][m & 3], 0, 0, 0); \
-      TILE_FENCE;                                                                                       \
-      if (m < 4) {                                                                                      \
-        TILE_READ(rst, rs, 1 - (q), 2 * m);                                                             \
-        TILE_READ(rst, rs, 1 - (q), 2 * m + 1);                                                         \
-      } else if (m < 12) {                                                                              \
-        if (fetch) TILE_LOAD(kt, dst, (x0) + m - 4);                                                    \
-      }                                                                                                 \
-      TILE_FENCE;                                                                                       \
-    }                                                                                                   \
+  // fragments q in use; the next step's from step rs of rst; loads x0 .. x0 + 2 W - 1 of stage kt into dst
+#define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                      \
+  do {                                                                                                 \
+    _Pragma("unroll") for (int m = 0; m < W * W; m++) {                                                \
+      acc[m / W][m % W] =                                                                              \
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q][m / W], vb[q][m % W], acc[m / W][m % W], 0, 0, 0); \
+      TILE_FENCE;                                                                                      \
+      if (m < W) {                                                                                     \
+        TILE_READ(rst, rs, 1 - (q), 2 * m);                                                            \
+        TILE_READ(rst, rs, 1 - (q), 2 * m + 1);                                                        \
+      } else if (W == 4 && m < 12) {                                                                   \
+        if (fetch) TILE_LOAD(kt, dst, (x0) + m - 4);                                                   \
+      } else if (W == 2) {                                                                             \
+        if (fetch) {                                                                                   \
+          TILE_LOAD(kt, dst, (x0) + 2 * m - 4);                                                        \
+          TILE_LOAD(kt, dst, (x0) + 2 * m - 3);                                                        \
+        }                                                                                              \
+      }                                                                                                \
+      TILE_FENCE;                                                                                      \
+    }                                                                                                  \
   } while (0)
   // the wait: this wave's reads of cur are complete and its part of nxt has landed
 #define TILE_STAGE_OF(kt, cur, nxt)                               \
   do {                                                            \
     const int k1 = min((kt) + 1, end - 1), k2 = min((kt) + 2, end - 1); \
-    TILE_STEP(0, cur, 1, true, k1, nxt, 8);                       \
+    TILE_STEP(0, cur, 1, true, k1, nxt, 2 * W);                       \
     TILE_STEP(1, cur, 2, false, 0, nxt, 0);                       \
     TILE_STEP(0, cur, 3, false, 0, nxt, 0);                       \
     asm volatile("" ::: "memory");                                \
@@ -275,20 +290,20 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
     TILE_STEP(1, nxt, 0, true, k2, cur, 0);                       \
   } while (0)
 #pragma unroll
-  for (int x = 0; x < 16; x++) TILE_LOAD(first, lds, x);
+  for (int x = 0; x < 4 * W; x++) TILE_LOAD(first, lds, x);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 #pragma unroll
-  for (int x = 0; x < 8; x++) TILE_READ(lds, 0, 0, x);
+  for (int x = 0; x < 2 * W; x++) TILE_READ(lds, 0, 0, x);
 #pragma unroll
-  for (int x = 0; x < 8; x++) TILE_LOAD(first + 1, lds + TILE_STAGE, x);
+  for (int x = 0; x < 2 * W; x++) TILE_LOAD(first + 1, lds + STAGE, x);
   // restrict (on arguments that the compiler cannot replace by their values)
   // lets it see that reads of one buffer do not wait for the fetch into the other
   auto pair = [&](int kt, uint8_t* __restrict__ b0, uint8_t* __restrict__ b1) {
     TILE_STAGE_OF(kt, b0, b1);
     TILE_STAGE_OF(kt + 1, b1, b0);
   };
-  uint32_t o0 = 0, o1 = TILE_STAGE;
+  uint32_t o0 = 0, o1 = STAGE;
   asm volatile("" : "+s"(o0), "+s"(o1));
   for (int kt = first; kt < end; kt += 2) pair(kt, lds + o0, lds + o1);
   // the clamped loads have landed before the caller uses the LDS
@@ -298,6 +313,55 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
 #undef TILE_LOAD
 #undef TILE_READ
 #undef TILE_FENCE
+}
+
+// The same for a few stages, kt of them from 0 on, through one LDS buffer (half
+// of tile_lds): nothing overlaps inside a workgroup, so it is for tiles of which
+// several share a compute unit.
+template <int W, bool AMAJ, bool BMAJ>
+__device__ __forceinline__ void tile_product_short(const TileOperand& a, const TileOperand& b, int kt, uint8_t* lds,
+                                                   floatx16 (&acc)[W][W]) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5;
+  TileFetch<W, AMAJ> fa;
+  TileFetch<W, BMAJ> fb;
+  fa.init(a, wave, lane);
+  fb.init(b, wave, lane);
+  TileFrag<W, AMAJ> ra;
+  TileFrag<W, BMAJ> rb;
+  ra.init((wave >> 1) * 32 * W, lane);
+  rb.init((wave & 1) * 32 * W, lane);
+#pragma unroll
+  for (int i = 0; i < W; i++)
+#pragma unroll
+    for (int j = 0; j < W; j++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+  for (int k = 0; k < kt; k++) {
+    if (k > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2 * W; j++) {
+      fa.issue(a, k, lds, wave, lane, j);
+      fb.issue(b, k, lds + tile_operand(W), wave, lane, j);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      bf16x8_t va[W], vb[W];
+#pragma unroll
+      for (int i = 0; i < W; i++) {
+        va[i] = ra.read(lds, i, s, h);
+        vb[i] = rb.read(lds + tile_operand(W), i, s, h);
+      }
+#pragma unroll
+      for (int i = 0; i < W; i++)
+#pragma unroll
+        for (int j = 0; j < W; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[i], vb[j], acc[i][j], 0, 0, 0);
+    }
+  }
 }
 
 // Tile (pm, pn) of workgroup bid in a grid of num_m x num_n tiles.  Workgroups

@@ -1,7 +1,7 @@
 // Softmax cross entropy of a linear head and its gradient
 // (nvfp4_linear_cross_entropy, nvfp4_linear_cross_entropy_backward), gfx950.
 //
-// Forward: the logits z = x W^T are formed in 256 x 256 tiles on the BF16 matrix
+// Forward: the logits z = x W^T are formed in tiles on the BF16 matrix
 // cores (bf16_tile.hpp); each tile leaves one (maximum, sum of exp(z - maximum))
 // pair per token, and the label's logit; a second kernel joins a token's pairs.
 // Backward, on the tokens that have a label only, over pieces of the vocabulary:
@@ -32,39 +32,41 @@ __device__ __forceinline__ int tile_row(int i, int r) { return 32 * i + 8 * (r >
 
 // stats[t][vt] = the pair of token t and vocabulary tile vt; zlab[t] = the
 // logit of t's label.
-__global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
+template <int W, bool EVEN>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
                                                                   const uint16_t* x, uint32_t ld_x, int T, int H,
                                                                   const int64_t* labels, float2* stats, float* zlab) {
   extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int TILE = tile_side(W), WAVE = 32 * W;
   int pm, pn;
   tile_place(blockIdx.x, (V + TILE - 1) / TILE, (T + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
-  floatx16 acc[4][4];
-  tile_product<false, false>(TileOperand{w + (int64_t)m0 * ld_w, ld_w, V - m0, H},
+  floatx16 acc[W][W];
+  tile_product<W, false, false, EVEN>(TileOperand{w + (int64_t)m0 * ld_w, ld_w, V - m0, H},
                              TileOperand{x + (int64_t)n0 * ld_x, ld_x, T - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
-  const int rows = V - m0 - wm * 128 - 4 * h;  // vocabulary rows from the lane's first
-  float2 st[4];
+  const int rows = V - m0 - wm * WAVE - 4 * h;  // vocabulary rows from the lane's first
+  float2 st[W];
 #pragma unroll
-  for (int j = 0; j < 4; j++) {
-    const int t = n0 + wn * 128 + 32 * j + lr;
+  for (int j = 0; j < W; j++) {
+    const int t = n0 + wn * WAVE + 32 * j + lr;
     if (V - m0 < TILE) {
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < W; i++)
 #pragma unroll
         for (int r = 0; r < 16; r++)
           if (tile_row(i, r) >= rows) acc[i][j][r] = -INFINITY;  // adds nothing below
     }
     // the label's row from the lane's first, where it is one of the wave's
     const int64_t label = t < T ? labels[t] : -1;
-    const int lab = label >= 0 && label < V ? (int)label - m0 - wm * 128 - 4 * h : -1;
-    if (__any(lab >= 0 && lab < 128)) {
+    const int lab = label >= 0 && label < V ? (int)label - m0 - wm * WAVE - 4 * h : -1;
+    if (__any(lab >= 0 && lab < WAVE)) {
       float z = 0.0f;
       bool mine = false;  // rows alternate in fours between the lanes of a column
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int i = 0; i < W; i++)
 #pragma unroll
         for (int r = 0; r < 16; r++) {
           z = lab == tile_row(i, r) ? acc[i][j][r] : z;
@@ -74,14 +76,14 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
     }
     float mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
       for (int r = 0; r < 16; r++) mx = fmaxf(mx, acc[i][j][r]);
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
     const float sh = shift_of(mx);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
       for (int r = 0; r < 16; r++) s += exp_fast(acc[i][j][r] - sh);
     s += __shfl_xor(s, 32, 64);
@@ -91,12 +93,12 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_stats(const uint16_t
   __syncthreads();
   float2* half = reinterpret_cast<float2*>(lds);
   if (wm == 1 && h == 0)
-    for (int j = 0; j < 4; j++) half[wn * 128 + 32 * j + lr] = st[j];
+    for (int j = 0; j < W; j++) half[wn * WAVE + 32 * j + lr] = st[j];
   __syncthreads();
   if (wm == 0 && h == 0)
-    for (int j = 0; j < 4; j++) {
-      const int t = n0 + wn * 128 + 32 * j + lr;
-      if (t < T) stats[(int64_t)t * ((V + TILE - 1) / TILE) + pm] = join(st[j], half[wn * 128 + 32 * j + lr]);
+    for (int j = 0; j < W; j++) {
+      const int t = n0 + wn * WAVE + 32 * j + lr;
+      if (t < T) stats[(int64_t)t * ((V + TILE - 1) / TILE) + pm] = join(st[j], half[wn * WAVE + 32 * j + lr]);
     }
 }
 
@@ -147,49 +149,53 @@ __global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, int64_t 
 }
 
 // xc[i] = x[list[i]] for the n labelled tokens (nothing else of x is read
-// again), then zeros up to a multiple of 64 rows (K of the dW product).
+// again), then zeros up to a multiple of 128 rows (K of the dw product).
 __global__ __launch_bounds__(256) void k_gather(const uint16_t* x, int64_t ld_x, int64_t H, Tokens tk, uint16_t* xc) {
   const int64_t i = blockIdx.x;
   const int n = *tk.n;
-  if (i >= (n + 63) / 64 * 64) return;
+  if (i >= (n + 127) / 128 * 128) return;
   const uint16_t* src = x + (i < n ? (int64_t)tk.list[i] * ld_x : 0);
   for (int64_t c = threadIdx.x * 8; c < H; c += 256 * 8)
     *reinterpret_cast<u32x4_t*>(xc + i * H + c) =
         i < n ? *reinterpret_cast<const u32x4_t*>(src + c) : u32x4_t{0, 0, 0, 0};
 }
 
-// ---- a BF16 tile through LDS: rows n of 256 values of m (512 bytes); the
-// 16-byte chunk g of row n lies in slot g ^ (n & 31), so that the 32 rows a wave
+// ---- a BF16 tile through LDS: rows n of 64 W values of m (8 W chunks of 16
+// bytes); chunk g of row n lies in slot g ^ (n mod 8 W), so that the rows a wave
 // writes at once fall into different banks.
 
 // Four consecutive values of m (from 8 g + 4 half) of row n.
+template <int W>
 __device__ __forceinline__ void tile_put(uint8_t* lds, int n, int g, int half, uint32_t lo, uint32_t hi) {
-  *reinterpret_cast<u32x2_t*>(lds + n * 512 + ((g ^ (n & 31)) << 4) + 8 * half) = u32x2_t{lo, hi};
+  *reinterpret_cast<u32x2_t*>(lds + n * 128 * W + ((g ^ (n & (8 * W - 1))) << 4) + 8 * half) = u32x2_t{lo, hi};
 }
+template <int W>
 __device__ __forceinline__ u32x4_t tile_get(const uint8_t* lds, int n, int g) {
-  return *reinterpret_cast<const u32x4_t*>(lds + n * 512 + ((g ^ (n & 31)) << 4));
+  return *reinterpret_cast<const u32x4_t*>(lds + n * 128 * W + ((g ^ (n & (8 * W - 1))) << 4));
 }
 
-// d^T of a piece of the vocabulary, BF16 [rows up to a multiple of 64][ldd], one
-// column per labelled token, zeros in the columns from n up to a multiple of 64
+// d^T of a piece of the vocabulary, BF16 [rows up to a multiple of 128][ldd], one
+// column per labelled token, zeros in the columns from n up to a multiple of 128
 // and in the rows past the piece's last: both are K of a later product.
-__global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
+template <int W, bool EVEN>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
                                                                  const uint16_t* xc, int H, int tiles_t, int64_t v_first,
                                                                  Tokens tk, const int64_t* labels, const float* lse,
                                                                  const float* dloss, uint16_t* d, int64_t ldd) {
   extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int n_tok = *tk.n;
   int pm, pn;  // token tile, vocabulary tile
   tile_place(blockIdx.x, tiles_t, (rows + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
   if (m0 >= n_tok) return;
-  floatx16 acc[4][4];
-  tile_product<false, false>(TileOperand{xc + (int64_t)m0 * H, (uint32_t)H, n_tok - m0, H},
+  floatx16 acc[W][W];
+  tile_product<W, false, false, EVEN>(TileOperand{xc + (int64_t)m0 * H, (uint32_t)H, n_tok - m0, H},
                              TileOperand{w + (int64_t)n0 * ld_w, ld_w, rows - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
   // what the tile's tokens hold: lse, dloss, and the label's row in this tile (or -1)
   __syncthreads();
-  float* s_lse = reinterpret_cast<float*>(lds + TILE_LDS);
+  float* s_lse = reinterpret_cast<float*>(lds + tile_lds(W));
   float* s_g = s_lse + TILE;
   int* s_lab = reinterpret_cast<int*>(s_g + TILE);
   if (threadIdx.x < TILE) {
@@ -209,22 +215,23 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
   __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
-  // a label of the wave's 128 tokens among its 128 vocabulary rows?
-  const int lab0 = s_lab[wm * 128 + lane] >> 7, lab1 = s_lab[wm * 128 + 64 + lane] >> 7;  // -1 stays -1
-  const bool hit = __any(lab0 == wn || lab1 == wn);
+  // a label of the wave's tokens among its vocabulary rows?  (-1 stays -1)
+  const int lab0 = s_lab[wm * WAVE + lane] / WAVE, lab1 = s_lab[wm * WAVE + WAVE - 64 + lane] / WAVE;
+  const bool hit = __any((s_lab[wm * WAVE + lane] >= 0 && lab0 == wn) ||
+                         (s_lab[wm * WAVE + WAVE - 64 + lane] >= 0 && lab1 == wn));
   auto put = [&](auto with_labels) {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int m = wm * 128 + 32 * i + 8 * q + 4 * h;
+        const int m = wm * WAVE + 32 * i + 8 * q + 4 * h;
         const float4 l = *reinterpret_cast<const float4*>(s_lse + m);
         const float4 g = *reinterpret_cast<const float4*>(s_g + m);
         int4 lab = make_int4(-1, -1, -1, -1);
         if constexpr (with_labels.value) lab = *reinterpret_cast<const int4*>(s_lab + m);
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const int n = wn * 128 + 32 * j + lr;
+        for (int j = 0; j < W; j++) {
+          const int n = wn * WAVE + 32 * j + lr;
           float p0 = exp_fast(acc[i][j][4 * q] - l.x), p1 = exp_fast(acc[i][j][4 * q + 1] - l.y);
           float p2 = exp_fast(acc[i][j][4 * q + 2] - l.z), p3 = exp_fast(acc[i][j][4 * q + 3] - l.w);
           if constexpr (with_labels.value) {
@@ -233,7 +240,7 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
             p2 -= lab.z == n ? 1.0f : 0.0f;
             p3 -= lab.w == n ? 1.0f : 0.0f;
           }
-          tile_put(lds, n, m >> 3, h, bf16_pack(p0 * g.x, p1 * g.y), bf16_pack(p2 * g.z, p3 * g.w));
+          tile_put<W>(lds, n, m >> 3, h, bf16_pack(p0 * g.x, p1 * g.y), bf16_pack(p2 * g.z, p3 * g.w));
         }
         __builtin_amdgcn_sched_barrier(0);  // few token values at a time beside 256 accumulators
       }
@@ -243,14 +250,14 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
   else
     put(std::false_type{});
   __syncthreads();
-  const int padded = (rows + 63) / 64 * 64;
-  for (int e = threadIdx.x; e < TILE * 32; e += TILE_THREADS) {
-    const int n = e >> 5, g = e & 31;
+  const int padded = (rows + 127) / 128 * 128;
+  for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
+    const int n = e / (8 * W), g = e % (8 * W);
     const int c = m0 + 8 * g;
     if (n0 + n >= padded || c >= ldd) continue;
     u32x4_t v = {0, 0, 0, 0};
     if (n0 + n < rows && c < n_tok) {
-      v = tile_get(lds, n, g);
+      v = tile_get<W>(lds, n, g);
       if (c + 8 > n_tok) {
 #pragma unroll
         for (int k = 0; k < 4; k++)
@@ -262,24 +269,30 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_logits_grad(const uint16_t*
 }
 
 // dw[v][h] (+)= sum over the labelled tokens of d^T[v][i] xc[i][h]
-template <typename OutT>
-__global__ __launch_bounds__(TILE_THREADS, 1) void k_dw(const uint16_t* xc, int H, const uint16_t* d, int64_t ldd,
+template <int W, typename OutT>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint16_t* xc, int H, const uint16_t* d, int64_t ldd,
                                                         int rows, Tokens tk, OutT* dw, int64_t ld_dw, int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int n_tok = *tk.n;
   int pm, pn;
   tile_place(blockIdx.x, (H + TILE - 1) / TILE, (rows + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
-  const int K = (n_tok + 63) / 64 * 64;
-  floatx16 acc[4][4];
-  if (K > 0) {
-    tile_product<true, false>(TileOperand{xc + m0, (uint32_t)H, H - m0, K},
-                              TileOperand{d + (int64_t)n0 * ldd, (uint32_t)ldd, rows - n0, K}, K, 0, K / TILE_K, lds, acc);
+  const int K = (n_tok + 127) / 128 * 128;
+  floatx16 acc[W][W];
+  constexpr bool SHORT = W == 2;  // few tokens: one LDS buffer, four workgroups per CU
+  if (SHORT || K > 0) {
+    const TileOperand ox{xc + m0, (uint32_t)H, H - m0, K};
+    const TileOperand od{d + (int64_t)n0 * ldd, (uint32_t)ldd, rows - n0, K};
+    if constexpr (SHORT)
+      tile_product_short<W, true, false>(ox, od, (n_tok + TILE_K - 1) / TILE_K, lds, acc);
+    else
+      tile_product<W, true, false, true>(ox, od, K, 0, K / TILE_K, lds, acc);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
-      for (int j = 0; j < 4; j++)
+      for (int j = 0; j < W; j++)
 #pragma unroll
         for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
   }
@@ -287,12 +300,12 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dw(const uint16_t* xc, int 
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 4; j++)
+  for (int j = 0; j < W; j++)
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int m = wm * 128 + 32 * i + 8 * q + 4 * h, n = wn * 128 + 32 * j + lr;
+        const int m = wm * WAVE + 32 * i + 8 * q + 4 * h, n = wn * WAVE + 32 * j + lr;
         const bool in = n0 + n < rows && m0 + m < H;  // H is a multiple of 8
         OutT* out = dw + (int64_t)(n0 + n) * ld_dw + m0 + m;
         float v[4];
@@ -315,57 +328,66 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dw(const uint16_t* xc, int 
             v[2] += bf16lo(old[1]);
             v[3] += bf16hi(old[1]);
           }
-          tile_put(lds, n, m >> 3, h, bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3]));
+          tile_put<W>(lds, n, m >> 3, h, bf16_pack(v[0], v[1]), bf16_pack(v[2], v[3]));
         }
       }
   if constexpr (sizeof(OutT) == 2) {
     __syncthreads();
-    for (int e = threadIdx.x; e < TILE * 32; e += TILE_THREADS) {
-      const int n = e >> 5, g = e & 31;
+    for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
+      const int n = e / (8 * W), g = e % (8 * W);
       if (n0 + n < rows && m0 + 8 * g < H)
-        *reinterpret_cast<u32x4_t*>(dw + (int64_t)(n0 + n) * ld_dw + m0 + 8 * g) = tile_get(lds, n, g);
+        *reinterpret_cast<u32x4_t*>(dw + (int64_t)(n0 + n) * ld_dw + m0 + 8 * g) = tile_get<W>(lds, n, g);
     }
   }
 }
 
-// sum[part][i][h] (+)= sum over the part's vocabulary rows of d^T[v][i] w[v][h]
-// (FP32): the piece's rows are split into `parts` contiguous ranges of stages.
-__global__ __launch_bounds__(TILE_THREADS, 1) void k_dx_sum(const uint16_t* w, uint32_t ld_w, int H, const uint16_t* d,
-                                                            int64_t ldd, int rows, int tiles_t, int parts, Tokens tk,
-                                                            float* sum, int64_t T, int accumulate) {
+// How the dx product of n labelled tokens is spread over `units` workgroups: its
+// K (the vocabulary rows, `pairs` of 128 of them in a piece) is split into as many
+// parts as the units allow, each at least 256 rows deep.  Part p's sums are
+// rows p * rows .. of the workspace, FP32.
+struct DxSplit {
+  int tiles, parts;
+  int64_t rows;
+  __device__ DxSplit(int n, int side, int tiles_h, int units, int pairs)
+      : tiles((n + side - 1) / side), rows((int64_t)tiles * side) {
+    parts = max(1, min(units / max(tiles * tiles_h, 1), pairs / 2));
+  }
+};
+
+// sum[part][i][h] (+)= sum over the part's vocabulary rows of d^T[v][i] w[v][h];
+// `rows` vocabulary rows in this piece, `piece` in the largest.
+template <int W>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const uint16_t* w, uint32_t ld_w, int H,
+                                                                         const uint16_t* d, int64_t ldd, int rows,
+                                                                         int piece, Tokens tk, float* sum,
+                                                                         int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int n_tok = *tk.n;
   const int tiles_h = (H + TILE - 1) / TILE;
+  const DxSplit sp(n_tok, TILE, tiles_h, gridDim.x, (piece + 127) / 128);
+  if ((int)blockIdx.x >= tiles_h * sp.tiles * sp.parts) return;
   int pm, pn;
-  tile_place(blockIdx.x, tiles_h, tiles_t * parts, pm, pn);
-  const int part = pn / tiles_t;
-  const int m0 = pm * TILE, n0 = (pn - part * tiles_t) * TILE;
-  if (n0 >= n_tok) return;
-  const int KT = (rows + TILE_K - 1) / TILE_K;
-  const int kt0 = (int)((int64_t)KT * part / parts), kt1 = (int)((int64_t)KT * (part + 1) / parts);
-  if (kt0 == kt1) {  // fewer stages than parts: nothing to add
-    if (accumulate) return;
-  }
-  floatx16 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-#pragma unroll
-      for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
-  if (kt0 < kt1)
-    tile_product<true, true>(TileOperand{w + m0, ld_w, H - m0, rows},
-                             TileOperand{d + n0, (uint32_t)ldd, (int)(ldd - n0), KT * TILE_K}, rows, kt0, kt1, lds, acc);
+  tile_place(blockIdx.x, tiles_h, sp.tiles * sp.parts, pm, pn);
+  const int part = pn / sp.tiles;
+  const int m0 = pm * TILE, n0 = (pn - part * sp.tiles) * TILE;
+  const int pairs = (rows + 127) / 128;
+  const int kt0 = (int)((int64_t)pairs * part / sp.parts) * 2, kt1 = (int)((int64_t)pairs * (part + 1) / sp.parts) * 2;
+  if (kt0 == kt1) return;  // in a last piece that is shorter: nothing to add
+  floatx16 acc[W][W];
+  tile_product<W, true, true, true>(TileOperand{w + m0, ld_w, H - m0, rows},
+                              TileOperand{d + n0, (uint32_t)ldd, (int)(ldd - n0), pairs * 128}, pairs * 128, kt0, kt1, lds,
+                              acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
-  float* out = sum + (int64_t)part * T * H;
+  float* out = sum + part * sp.rows * H;
 #pragma unroll
-  for (int j = 0; j < 4; j++)
+  for (int j = 0; j < W; j++)
 #pragma unroll
-    for (int i = 0; i < 4; i++)
+    for (int i = 0; i < W; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
-        const int m = m0 + wm * 128 + 32 * i + 8 * q + 4 * h, n = n0 + wn * 128 + 32 * j + lr;
+        const int m = m0 + wm * WAVE + 32 * i + 8 * q + 4 * h, n = n0 + wn * WAVE + 32 * j + lr;
         if (n >= n_tok || m >= H) continue;
         float4* o = reinterpret_cast<float4*>(out + (int64_t)n * H + m);
         float4 s = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
@@ -374,27 +396,30 @@ __global__ __launch_bounds__(TILE_THREADS, 1) void k_dx_sum(const uint16_t* w, u
           s = make_float4(old.x + s.x, old.y + s.y, old.z + s.z, old.w + s.w);
         }
         *o = s;
+        if (q == 3) __builtin_amdgcn_sched_barrier(0);  // few old values at a time beside 256 accumulators
       }
 }
 
-// dx (BF16) from its FP32 sums, added in order; 0 for ignored tokens
-__global__ __launch_bounds__(256) void k_dx(const float* sum, int parts, int64_t T, int64_t H, Tokens tk, uint16_t* dx,
-                                            int64_t ld) {
+// dx (BF16) from its FP32 sums, added in order; 0 for ignored tokens.  A
+// workgroup takes 1024 columns of a token.
+__global__ __launch_bounds__(256) void k_dx(const float* sum, int units, int side, int pairs, int H, Tokens tk,
+                                            uint16_t* dx, int64_t ld) {
   const int64_t t = blockIdx.x;
   const int64_t i = tk.place[t];
-  for (int64_t c = threadIdx.x * 8; c < H; c += 256 * 8) {
-    float f[8];
-#pragma unroll
-    for (int q = 0; q < 8; q++) f[q] = 0.0f;
-    if (i >= 0)
-      for (int p = 0; p < parts; p++) {
-        const float4* s = reinterpret_cast<const float4*>(sum + (p * T + i) * H + c);
-        const float4 a = s[0], b = s[1];
-        f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
-        f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
-      }
-    *reinterpret_cast<u32x4_t*>(dx + t * ld + c) = VecOf<uint16_t>::pack(f);
+  const DxSplit sp(*tk.n, side, (H + side - 1) / side, units, pairs);
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= H) return;
+  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (i >= 0) {
+    const float4* p = reinterpret_cast<const float4*>(sum + i * H + c);
+    const int64_t step = sp.rows * H / 4;
+#pragma unroll 8
+    for (int q = 0; q < sp.parts; q++) {
+      const float4 v = p[q * step];
+      f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
+    }
   }
+  *reinterpret_cast<u32x2_t*>(dx + t * ld + c) = u32x2_t{bf16_pack(f.x, f.y), bf16_pack(f.z, f.w)};
 }
 
 __global__ __launch_bounds__(256) void k_zero(void* p, int64_t row_bytes, int64_t ld_bytes) {
@@ -407,25 +432,54 @@ int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 
 // Vocabulary rows per backward piece: d of a piece takes up to 512 MiB.
 constexpr int64_t kPieceBytes = int64_t(512) << 20;
-int64_t up64(int64_t n) { return (n + 63) / 64 * 64; }
-int64_t tiles_of(int64_t n) { return (n + TILE - 1) / TILE; }
+int64_t up128(int64_t n) { return (n + 127) / 128 * 128; }
+int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
 int64_t piece_rows(int64_t T, int64_t V) {
-  const int64_t r = std::max<int64_t>(kPieceBytes / (2 * up64(T)) / TILE * TILE, TILE);
+  const int64_t r = std::max<int64_t>(kPieceBytes / (2 * up128(T)) / 256 * 256, 256);
   return std::min(r, V);
 }
 
-// Parts of the dx product's K (a piece's vocabulary rows): as many as fill the
-// compute units of a 256-CU MI355X best, each at least 8 stages deep, at most 16.
-int64_t dx_parts(int64_t T, int64_t H, int64_t piece) {
-  const int64_t tiles = tiles_of(T) * tiles_of(H), stages = (piece + TILE_K - 1) / TILE_K;
-  int64_t best = 1;
-  double best_cost = 1e30;
-  for (int64_t s = 1; s <= 16 && (s == 1 || stages / s >= 8); s++) {
-    // rounds of workgroups times the stages of one, plus the store of its FP32 tile (about 8 stages' time)
-    const double cost = (double)((tiles * s + 255) / 256) * ((double)stages / s + 8.0);
-    if (cost < best_cost * 0.98) {
-      best_cost = cost;
-      best = s;
+// Tile size of an M x N product with K values of k: the one whose rounds of
+// workgroups over a 256-CU MI355X (one large tile per CU, two small ones) take
+// less.  Measured (H = 5120 and 2048, V = 10000 .. 131072, T = 64 .. 1000): a round
+// of large tiles takes 1.55 us a stage and 10 us around them, one of small tiles
+// 1.05 and 4, or 0.75 a stage where each has its CU to itself.
+double round_us(int64_t tiles, double stages, int W) {
+  if (W == 4) return (double)((tiles + 255) / 256) * (stages * 1.55 + 10.0);
+  const int64_t rest = tiles % 512;
+  return (double)(tiles / 512) * (stages * 1.05 + 4.0) +
+         (rest == 0 ? 0.0 : stages * (rest <= 256 ? 0.75 : 1.05) + 4.0);
+}
+int tile_w(int64_t M, int64_t N, int64_t K) {
+  const double stages = (double)((K + TILE_K - 1) / TILE_K);
+  const double large = round_us(tiles_of(M, 4) * tiles_of(N, 4), stages, 4);
+  return large <= round_us(tiles_of(M, 2) * tiles_of(N, 2), stages, 2) ? 4 : 2;
+}
+
+// Up to here the dw product has few enough stages that four small tiles per CU,
+// each unpipelined, beat one large tile (131072 x 5120: 0.63 against 0.76 ms at 256
+// tokens, 1.49 against 1.59 at 1000, 2.75 against 2.61 at 2000).
+constexpr int64_t SHORT_DW_TOKENS = 1536;
+
+// Workgroups of the dx product: its tiles are as few as T x H gives, so K (a
+// piece's vocabulary rows) is split, by the rounds that cost least.
+struct DxPlan {
+  int W;
+  int64_t units;
+};
+DxPlan dx_plan(int64_t T, int64_t H, int64_t piece) {
+  const int64_t stages = (piece + TILE_K - 1) / TILE_K;
+  DxPlan best{4, 0};
+  double best_us = 1e30;
+  for (int W = 4; W >= 2; W -= 2) {
+    const int64_t slots = W == 4 ? 256 : 512, tiles = tiles_of(T, W) * tiles_of(H, W);
+    for (int64_t r = 1; r <= 4 || r * slots < 2 * tiles + slots; r++) {
+      const int64_t parts = std::max<int64_t>(1, std::min(r * slots / tiles, stages / 4));
+      const double us = round_us(tiles * parts, (double)stages / parts, W);
+      if (us < best_us * 0.97) {
+        best_us = us;
+        best = DxPlan{W, std::max(r * slots, tiles)};
+      }
     }
   }
   return best;
@@ -433,74 +487,83 @@ int64_t dx_parts(int64_t T, int64_t H, int64_t piece) {
 
 // The backward workspace: offsets of its parts.
 struct BackPlan {
-  int64_t piece, ldd, parts;
-  int64_t dt, d, xc, sum, tok, end;
+  int64_t piece, ldd;
+  DxPlan dxp;
+  int64_t d, xc, sum, tok, end;
 };
 BackPlan back_plan(int64_t T, int64_t V, int64_t H) {
   BackPlan p;
-  p.dt = 0;
-  if (T <= FEW_TOKENS) {  // the whole vocabulary at once, d in both orientations
-    p.piece = V;
-    p.ldd = few_ldt(T);
-    p.parts = few_dx_parts(T, V, H);
-    p.d = up16(few_rows(V) * p.ldd * 2);
-    p.xc = p.d + up16(few_tokens(T) * few_rows(V) * 2);
-  } else {
-    p.piece = piece_rows(T, V);
-    p.ldd = up64(T);
-    p.parts = dx_parts(T, H, p.piece);
-    p.d = p.xc = up16(up64(p.piece) * p.ldd * 2);
-  }
-  p.sum = p.xc + up16(up64(T) * H * 2);
-  p.tok = p.sum + up16(p.parts * T * H * 4);
+  p.piece = piece_rows(T, V);
+  p.ldd = up128(T);
+  p.dxp = dx_plan(T, H, p.piece);
+  p.d = 0;
+  p.xc = up16(up128(p.piece) * p.ldd * 2);
+  p.sum = p.xc + up16(up128(T) * H * 2);
+  p.tok = p.sum + up16(p.dxp.units * tile_side(p.dxp.W) * tile_side(p.dxp.W) * 4);
   p.end = p.tok + up16((2 * T + 1) * 4);
   return p;
 }
 
-// Vocabulary tiles of the forward's pairs.
-int64_t stats_tiles(int64_t T, int64_t V) { return T <= FEW_TOKENS ? few_rows(V) / FEW_ROWS : tiles_of(V); }
-
-// Largest dynamic LDS of every tile kernel, set once.
-constexpr int kTileLds = TILE_LDS + 3 * TILE * 4;
-hipError_t allow_lds() {
+// Dynamic LDS of a tile kernel: its stages and the token values of a tile.
+constexpr int lds_of(int W) { return tile_lds(W) + 3 * tile_side(W) * 4; }
+hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
   static std::once_flag once;
   static hipError_t err = hipSuccess;
   std::call_once(once, [] {
-    const void* fns[] = {reinterpret_cast<const void*>(&k_logits_stats), reinterpret_cast<const void*>(&k_logits_grad),
-                         reinterpret_cast<const void*>(&k_dw<uint16_t>), reinterpret_cast<const void*>(&k_dw<float>),
-                         reinterpret_cast<const void*>(&k_dx_sum)};
-    for (const void* f : fns)
-      if (err == hipSuccess) err = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds);
+    auto allow = [](const void* f, int W) {
+      if (err == hipSuccess) err = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds_of(W));
+    };
+    allow(reinterpret_cast<const void*>(&k_logits_stats<4, true>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<4, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<4, true>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<4, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_dw<4, uint16_t>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, float>), 4);
+    allow(reinterpret_cast<const void*>(&k_dx_sum<4>), 4);
+    allow(reinterpret_cast<const void*>(&k_dx_sum<2>), 2);
   });
   return err;
+}
+
+// f(W, EVEN) with the tile size, and whether K is a whole number of pairs of
+// stages, as constants
+template <typename F>
+hipError_t with_tile(int W, bool even, F&& f) {
+  using std::integral_constant;
+  if (W == 4)
+    even ? f(integral_constant<int, 4>{}, std::true_type{}) : f(integral_constant<int, 4>{}, std::false_type{});
+  else
+    even ? f(integral_constant<int, 2>{}, std::true_type{}) : f(integral_constant<int, 2>{}, std::false_type{});
+  return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t linear_ce_workspace(int64_t T, int64_t V, int64_t H, bool train) {
-  const int64_t fwd = up16(stats_tiles(T, V) * T * 8) + up16(T * 4);
+  const int64_t fwd = up16(tiles_of(V, tile_w(V, T, H)) * T * 8) + up16(T * 4);
   return train ? std::max(fwd, back_plan(T, V, H).end) : fwd;
 }
 
 hipError_t launch_linear_ce(int64_t T, int64_t V, int64_t H, const void* x, int64_t ld_x, const void* w, int64_t ld_w,
                             const int64_t* labels, float* loss, float* lse, void* workspace, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int tiles = (int)stats_tiles(T, V);
-  float2* stats = static_cast<float2*>(workspace);
-  float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16((int64_t)tiles * T * 8));
-  const uint16_t* wp = static_cast<const uint16_t*>(w);
-  const uint16_t* xp = static_cast<const uint16_t*>(x);
-  hipError_t e;
-  if (T <= FEW_TOKENS) {
-    e = few_stats(wp, (uint32_t)ld_w, V, xp, (uint32_t)ld_x, T, H, labels, stats, zlab, s);
-  } else {
-    if ((e = allow_lds()) != hipSuccess) return e;
-    k_logits_stats<<<(unsigned)(tiles * tiles_of(T)), TILE_THREADS, kTileLds, s>>>(
-        wp, (uint32_t)ld_w, (int)V, xp, (uint32_t)ld_x, (int)T, (int)H, labels, stats, zlab);
-    e = hipGetLastError();
-  }
+  hipError_t e = allow_lds();
   if (e != hipSuccess) return e;
-  k_loss<<<(unsigned)T, 256, 0, s>>>(stats, tiles, (int)V, labels, zlab, loss, lse);
+  const int w_tile = tile_w(V, T, H);
+  const int64_t tiles = tiles_of(V, w_tile);
+  float2* stats = static_cast<float2*>(workspace);
+  float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16(tiles * T * 8));
+  e = with_tile(w_tile, H % 128 == 0, [&](auto W, auto even) {
+    k_logits_stats<W.value, even.value><<<(unsigned)(tiles * tiles_of(T, W.value)), TILE_THREADS, lds_of(W.value), s>>>(
+        static_cast<const uint16_t*>(w), (uint32_t)ld_w, (int)V, static_cast<const uint16_t*>(x), (uint32_t)ld_x, (int)T,
+        (int)H, labels, stats, zlab);
+  });
+  if (e != hipSuccess) return e;
+  k_loss<<<(unsigned)T, 256, 0, s>>>(stats, (int)tiles, (int)V, labels, zlab, loss, lse);
   return hipGetLastError();
 }
 
@@ -514,61 +577,58 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     k_zero<<<(unsigned)V, 256, 0, s>>>(dw, H * es, ld_dw * es);
     return hipGetLastError();
   }
+  hipError_t e = allow_lds();
+  if (e != hipSuccess) return e;
   const BackPlan pl = back_plan(T, V, H);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.dt);  // d^T
+  uint16_t* d = reinterpret_cast<uint16_t*>(ws + pl.d);  // d^T
   uint16_t* xc = reinterpret_cast<uint16_t*>(ws + pl.xc);
   float* sum = reinterpret_cast<float*>(ws + pl.sum);
   int* tok = reinterpret_cast<int*>(ws + pl.tok);
   const Tokens tk{tok, tok + 1, tok + 1 + T};
   k_tokens<<<1, 1024, 0, s>>>(labels, T, V, tk);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_gather<<<(unsigned)up64(T), 256, 0, s>>>(static_cast<const uint16_t*>(x), ld_x, H, tk, xc);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (T <= FEW_TOKENS) {
-    uint16_t* dr = reinterpret_cast<uint16_t*>(ws + pl.d);
-    const uint16_t* wp = static_cast<const uint16_t*>(w);
-    e = few_grad(wp, (uint32_t)ld_w, V, xc, T, H, tk, labels, lse, dloss, d, dr, s);
-    if (e == hipSuccess && dw != nullptr)
-      e = few_dw(xc, H, d, pl.ldd, V, T, tk, dw, dw_dt, ld_dw, accumulate, s);
-    if (e == hipSuccess && dx != nullptr) e = few_dx(wp, (uint32_t)ld_w, V, dr, T, H, tk, sum, s);
-    if (e != hipSuccess) return e;
-    if (dx != nullptr)
-      k_dx<<<(unsigned)T, 256, 0, s>>>(sum, (int)pl.parts, T, H, tk, static_cast<uint16_t*>(dx), ld_dx);
-    return hipGetLastError();
-  }
-  if ((e = allow_lds()) != hipSuccess) return e;
-  const int tt = (int)tiles_of(T);
-  const int64_t th = tiles_of(H);
+  k_gather<<<(unsigned)up128(T), 256, 0, s>>>(static_cast<const uint16_t*>(x), ld_x, H, tk, xc);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
     const int64_t n = std::min(pl.piece, V - v0);
-    const int64_t tv = tiles_of(n);
     const uint16_t* wp = static_cast<const uint16_t*>(w) + v0 * ld_w;
-    k_logits_grad<<<(unsigned)(tt * tv), TILE_THREADS, kTileLds, s>>>(wp, (uint32_t)ld_w, (int)n, xc, (int)H, tt, v0,
-                                                                      tk, labels, lse, dloss, d, pl.ldd);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (dw != nullptr && T <= FEW_DW_TOKENS) {
-      void* out = static_cast<uint8_t*>(dw) + v0 * ld_dw * (dw_dt == 0 ? 2 : 4);
-      if ((e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, s)) != hipSuccess) return e;
-    } else if (dw != nullptr) {
-      if (dw_dt == 0)
-        k_dw<<<(unsigned)(th * tv), TILE_THREADS, kTileLds, s>>>(
-            xc, (int)H, d, pl.ldd, (int)n, tk, static_cast<uint16_t*>(dw) + v0 * ld_dw, ld_dw, accumulate);
-      else
-        k_dw<<<(unsigned)(th * tv), TILE_THREADS, kTileLds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk,
-                                                                 static_cast<float*>(dw) + v0 * ld_dw, ld_dw,
-                                                                 accumulate);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = with_tile(tile_w(T, n, H), H % 128 == 0, [&](auto W, auto even) {
+      const int64_t tt = tiles_of(T, W.value), tv = tiles_of(n, W.value);
+      k_logits_grad<W.value, even.value><<<(unsigned)(tt * tv), TILE_THREADS, lds_of(W.value), s>>>(
+          wp, (uint32_t)ld_w, (int)n, xc, (int)H, (int)tt, v0, tk, labels, lse, dloss, d, pl.ldd);
+    });
+    if (e != hipSuccess) return e;
+    if (dw != nullptr) {
+      uint8_t* out = static_cast<uint8_t*>(dw) + v0 * ld_dw * (dw_dt == 0 ? 2 : 4);
+      if (T <= FEW_DW_TOKENS) {
+        e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, s);
+      } else {
+        e = with_tile(T <= SHORT_DW_TOKENS ? 2 : 4, true, [&](auto W, auto) {
+          const unsigned grid = (unsigned)(tiles_of(H, W.value) * tiles_of(n, W.value));
+          const int lds = W.value == 2 ? tile_lds(2) / 2 : lds_of(W.value);
+          if (dw_dt == 0)
+            k_dw<W.value><<<grid, TILE_THREADS, lds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk,
+                                                                 reinterpret_cast<uint16_t*>(out), ld_dw, accumulate);
+          else
+            k_dw<W.value><<<grid, TILE_THREADS, lds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk,
+                                                                 reinterpret_cast<float*>(out), ld_dw, accumulate);
+        });
+      }
+      if (e != hipSuccess) return e;
     }
     if (dx != nullptr) {
-      k_dx_sum<<<(unsigned)(th * tt * pl.parts), TILE_THREADS, kTileLds, s>>>(
-          wp, (uint32_t)ld_w, (int)H, d, pl.ldd, (int)n, tt, (int)pl.parts, tk, sum, T, v0 > 0 ? 1 : 0);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
+      e = with_tile(pl.dxp.W, true, [&](auto W, auto) {
+        k_dx_sum<W.value><<<(unsigned)pl.dxp.units, TILE_THREADS, lds_of(W.value), s>>>(
+            wp, (uint32_t)ld_w, (int)H, d, pl.ldd, (int)n, (int)pl.piece, tk, sum, v0 > 0 ? 1 : 0);
+      });
+      if (e != hipSuccess) return e;
     }
   }
   if (dx == nullptr) return hipSuccess;
-  k_dx<<<(unsigned)T, 256, 0, s>>>(sum, (int)pl.parts, T, H, tk, static_cast<uint16_t*>(dx), ld_dx);
+  k_dx<<<dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), 256, 0, s>>>(
+      sum, (int)pl.dxp.units, tile_side(pl.dxp.W), (int)((pl.piece + 127) / 128), (int)H, tk, static_cast<uint16_t*>(dx),
+      ld_dx);
   return hipGetLastError();
 }
 
