@@ -34,6 +34,12 @@ struct VecOf<uint16_t> {
   static constexpr int N = 8;
   static __device__ __forceinline__ u32x4_t load(const uint16_t* p) { return *reinterpret_cast<const u32x4_a2*>(p); }
   static __device__ __forceinline__ void store(uint16_t* p, u32x4_t v) { *reinterpret_cast<u32x4_a2*>(p) = v; }
+  static __device__ __forceinline__ u32x4_t load_nt(const uint16_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+  }
+  static __device__ __forceinline__ void store_nt(uint16_t* p, u32x4_t v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+  }
   // the first n < 8 elements, the rest zero
   static __device__ __forceinline__ u32x4_t load_n(const uint16_t* p, int n) {
     u32x4_t v = {0, 0, 0, 0};
@@ -65,6 +71,12 @@ struct VecOf<float> {
   static constexpr int N = 4;
   static __device__ __forceinline__ u32x4_t load(const float* p) { return *reinterpret_cast<const u32x4_a4*>(p); }
   static __device__ __forceinline__ void store(float* p, u32x4_t v) { *reinterpret_cast<u32x4_a4*>(p) = v; }
+  static __device__ __forceinline__ u32x4_t load_nt(const float* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
+  }
+  static __device__ __forceinline__ void store_nt(float* p, u32x4_t v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a4*>(p));
+  }
   static __device__ __forceinline__ u32x4_t load_n(const float* p, int n) {
     u32x4_t v = {0, 0, 0, 0};
 #pragma unroll
@@ -87,16 +99,16 @@ struct VecOf<float> {
   static __device__ __forceinline__ float one(const float* p) { return *p; }
 };
 
-// n elements (n <= 0: none, n >= N: a whole vector) at p
-template <typename T>
+// n elements (n <= 0: none, n >= N: a whole vector) at p.  STREAM: past the caches.
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ u32x4_t load_vec(const T* p, int n) {
-  if (n >= VecOf<T>::N) return VecOf<T>::load(p);
+  if (n >= VecOf<T>::N) return STREAM ? VecOf<T>::load_nt(p) : VecOf<T>::load(p);
   return VecOf<T>::load_n(p, n);
 }
-template <typename T>
+template <typename T, bool STREAM = false>
 __device__ __forceinline__ void store_vec(T* p, u32x4_t v, int n) {
   if (n >= VecOf<T>::N)
-    VecOf<T>::store(p, v);
+    STREAM ? VecOf<T>::store_nt(p, v) : VecOf<T>::store(p, v);
   else
     VecOf<T>::store_n(p, v, n);
 }
@@ -116,26 +128,35 @@ inline Dropout make_dropout(float p, uint64_t seed) {
 }
 
 // Dropout of N (4 or 8) consecutive elements from index i0: each hash word
-// covers an even element (low half) and the odd one after it (high half).
+// covers an even element (low half) and the odd one after it (high half).  Where
+// i0 is a multiple of N the N / 2 pairs differ in their low bits only, which then
+// come out of the hash's first product as a uniform term: one multiply for all.
 template <int N>
 __device__ __forceinline__ void drop(float* v, uint32_t i0, const Dropout& d) {
+  constexpr uint32_t LOW = N / 2 - 1;
   const uint32_t pair = i0 >> 1;
-  if ((i0 & 1u) == 0) {
+  if ((i0 & (N - 1)) == 0) {
+    uint32_t base = ((d.key ^ pair) & ~LOW) * 747796405u;
+    asm volatile("" : "+v"(base));  // keep the shared product
 #pragma unroll
-    for (int q = 0; q < N / 2; q++) {
-      const uint32_t h = pcg_host(d.key ^ (pair + q));
+    for (uint32_t q = 0; q < N / 2; q++) {
+      const uint32_t h = pcg_tail(base + (((d.key & LOW) ^ q) * 747796405u + 2891336453u));
       v[2 * q] = (h & 0xFFFFu) >= d.cut ? v[2 * q] * d.scale : 0.0f;
       v[2 * q + 1] = (h >> 16) >= d.cut ? v[2 * q + 1] * d.scale : 0.0f;
     }
-  } else {
-    uint32_t h = pcg_host(d.key ^ pair);
+    return;
+  }
+  // an odd i0 starts with the high half of its pair
+  uint32_t h = pcg_host(d.key ^ pair);
+  const bool odd = (i0 & 1u) != 0;
 #pragma unroll
-    for (int q = 0; q < N / 2; q++) {
-      const uint32_t g = pcg_host(d.key ^ (pair + q + 1));
-      v[2 * q] = (h >> 16) >= d.cut ? v[2 * q] * d.scale : 0.0f;
-      v[2 * q + 1] = (g & 0xFFFFu) >= d.cut ? v[2 * q + 1] * d.scale : 0.0f;
-      h = g;
-    }
+  for (uint32_t q = 0; q < N / 2; q++) {
+    uint32_t g = h;
+    if (odd || q + 1 < N / 2) g = pcg_host(d.key ^ (pair + q + 1));
+    const uint32_t b0 = odd ? h >> 16 : h & 0xFFFFu, b1 = odd ? g & 0xFFFFu : h >> 16;
+    v[2 * q] = b0 >= d.cut ? v[2 * q] * d.scale : 0.0f;
+    v[2 * q + 1] = b1 >= d.cut ? v[2 * q + 1] * d.scale : 0.0f;
+    h = g;
   }
 }
 

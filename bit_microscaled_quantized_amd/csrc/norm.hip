@@ -8,9 +8,10 @@
 // registers hold is read twice instead.
 //
 // A group of G lanes takes one row, lane j its 16-byte vectors j, j + G, ...
-// (8 BF16 or 4 FP32 elements): narrow rows share a wave or a workgroup, wide
-// ones take up to 1024 lanes.  Sums are FP32: each lane adds its own elements,
-// lanes are added by a butterfly, waves through LDS, always in the same order.
+// (8 BF16 or 4 FP32 elements), up to VPT of them.  G is 16 or 32, where several
+// rows share a wave, or a multiple of 64, chosen per launch to fit the row.  Sums
+// are FP32: each lane adds its own elements, lanes are added by a butterfly, waves
+// through LDS, always in the same order.
 #include "layers_device.hpp"
 #include "layers_launch.hpp"
 
@@ -20,19 +21,19 @@ namespace {
 
 constexpr int MXB = 32;  // columns per block of the 8-bit output
 
-// Sum over the G lanes of a group (G <= 64: inside a wave; G > 64: the whole
-// workgroup, through red[G / 64]); every lane gets the result.
-template <int G>
-__device__ __forceinline__ float group_sum(float v, float* red) {
-#pragma unroll
-  for (int m = 1; m < (G < 64 ? G : 64); m <<= 1) v += __shfl_xor(v, m, 64);
-  if constexpr (G > 64) {
+// Sum over the G lanes of a group (inside a wave, or through the group's G / 64
+// places in red, one per wave of the workgroup); every lane gets the result.  All
+// lanes of the workgroup call it together.
+__device__ __forceinline__ float group_sum(float v, int G, float* red) {
+  const int span = min(G, 64);
+  for (int m = 1; m < span; m <<= 1) v += __shfl_xor(v, m, 64);
+  if (G > 64) {
     __syncthreads();  // the last use of red is over
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
+    const int waves = G / 64, first = (int)threadIdx.x / G * waves;
     v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < G / 64; w++) v += red[w];
+    for (int w = 0; w < waves; w++) v += red[first + w];
   }
   return v;
 }
@@ -151,46 +152,50 @@ __device__ __forceinline__ void store_mx8(const float* f, uint32_t c, int n, uin
 
 // h = residual + dropout(x) of one vector
 template <typename T>
-__device__ __forceinline__ void sum_vec(const NormArgs& a, const T* xr, const T* rr, uint32_t row, uint32_t c, int n,
-                                        float* h) {
+__device__ __forceinline__ void sum_vec(const NormArgs& a, u32x4_t x, u32x4_t r, uint32_t row, uint32_t c, float* h) {
   constexpr int N = VecOf<T>::N;
-  VecOf<T>::unpack(load_vec(xr + c, n), h);
+  VecOf<T>::unpack(x, h);
   if (a.drop.cut != 0) drop<N>(h, row * a.cols + c, a.drop);
   if (a.residual != nullptr) {
-    float r[N];
-    VecOf<T>::unpack(load_vec(rr + c, n), r);
+    float f[N];
+    VecOf<T>::unpack(r, f);
 #pragma unroll
-    for (int i = 0; i < N; i++) h[i] = r[i] + h[i];
+    for (int i = 0; i < N; i++) h[i] = f[i] + h[i];
   }
 }
 
-// Rows of up to G * VPT vectors, held in registers.
-template <typename T, int G, int VPT, bool MX>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_rms_norm(NormArgs a) {
+// Rows of up to G * VPT vectors, held in registers; all of a row's loads are in
+// flight at once.
+template <typename T, int VPT, bool MX, bool STREAM>
+__global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a, int G) {
   constexpr int N = VecOf<T>::N;
-  constexpr int NT = G < 256 ? 256 : G;
-  __shared__ float red[NT / 64];
-  const uint32_t row = blockIdx.x * (NT / G) + threadIdx.x / G;
+  __shared__ float red[16];
+  const uint32_t row = blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
   const uint32_t j = threadIdx.x % G;
   const bool live = row < a.rows;
   const T* xr = static_cast<const T*>(a.x) + (int64_t)row * a.ld_x;
   const T* rr = static_cast<const T*>(a.residual) + (int64_t)row * a.ld_r;
-  float h[VPT][N];
-  float sq = 0.0f;
+  u32x4_t vx[VPT], vr[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const uint32_t c = (j + k * G) * N;
     const int n = live ? (int)a.cols - (int)c : 0;
-#pragma unroll
-    for (int i = 0; i < N; i++) h[k][i] = 0.0f;
+    vx[k] = vr[k] = u32x4_t{0, 0, 0, 0};
     if (n > 0) {
-      sum_vec<T>(a, xr, rr, row, c, n, h[k]);
-      // elements past the row's end were loaded as zeros and stay zeros
+      vx[k] = load_vec<T, STREAM>(xr + c, n);
+      if (a.residual != nullptr) vr[k] = load_vec<T, STREAM>(rr + c, n);
     }
+  }
+  float h[VPT][N];
+  float sq = 0.0f;
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    // elements past the row's end were loaded as zeros and stay zeros
+    sum_vec<T>(a, vx[k], vr[k], row, (j + k * G) * N, h[k]);
 #pragma unroll
     for (int i = 0; i < N; i++) sq += h[k][i] * h[k][i];
   }
-  sq = group_sum<G>(sq, red);
+  sq = group_sum(sq, G, red);
   const float rstd = 1.0f / sqrtf(sq / (float)a.cols + a.eps);
   if (live && j == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
@@ -198,7 +203,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_rms_norm(NormArgs a) {
     const uint32_t c = (j + k * G) * N;
     const int n = live ? (int)a.cols - (int)c : 0;
     if (n > 0 && a.h != nullptr)
-      store_vec(static_cast<T*>(a.h) + (int64_t)row * a.ld_h + c, VecOf<T>::pack(h[k]), n);
+      store_vec<T, STREAM>(static_cast<T*>(a.h) + (int64_t)row * a.ld_h + c, VecOf<T>::pack(h[k]), n);
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; i++) g[i] = 0.0f;
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_rms_norm(NormArgs a) {
       const uint32_t blocks = (a.cols + MXB - 1) / MXB;
       store_mx8<N>(h[k], c, n, a.codes + (int64_t)row * a.cols, a.scales + (int64_t)row * blocks);
     } else {
-      if (n > 0) store_vec(static_cast<T*>(a.y) + (int64_t)row * a.ld_y + c, VecOf<T>::pack(h[k]), n);
+      if (n > 0) store_vec<T, STREAM>(static_cast<T*>(a.y) + (int64_t)row * a.ld_y + c, VecOf<T>::pack(h[k]), n);
     }
   }
 }
@@ -228,12 +233,13 @@ __global__ __launch_bounds__(1024) void k_rms_norm_wide(NormArgs a) {
     const int n = (int)min((int64_t)N, (int64_t)a.cols - c);
     if (n <= 0) continue;
     float h[N], s = 0.0f;
-    sum_vec<T>(a, xr, rr, row, (uint32_t)c, n, h);
+    sum_vec<T>(a, load_vec(xr + c, n), a.residual == nullptr ? u32x4_t{0, 0, 0, 0} : load_vec(rr + c, n), row,
+               (uint32_t)c, h);
 #pragma unroll
     for (int i = 0; i < N; i++) s += h[i] * h[i];
     sq += s;
   }
-  sq = group_sum<1024>(sq, red);
+  sq = group_sum(sq, 1024, red);
   const float rstd = 1.0f / sqrtf(sq / (float)a.cols + a.eps);
   if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
   for (uint64_t base = 0; base < a.cols; base += 1024 * N) {
@@ -243,7 +249,8 @@ __global__ __launch_bounds__(1024) void k_rms_norm_wide(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; i++) h[i] = g[i] = 0.0f;
     if (n > 0) {
-      sum_vec<T>(a, xr, rr, row, (uint32_t)c, n, h);
+      sum_vec<T>(a, load_vec(xr + c, n), a.residual == nullptr ? u32x4_t{0, 0, 0, 0} : load_vec(rr + c, n), row,
+                 (uint32_t)c, h);
       load_gamma<N>(a.gamma, a.gamma_f32, (uint32_t)c, n, g);
       if (a.h != nullptr) store_vec(static_cast<T*>(a.h) + (int64_t)row * a.ld_h + c, VecOf<T>::pack(h), n);
     }
@@ -275,104 +282,126 @@ struct NormBackArgs {
   Dropout drop;
 };
 
-// g of one vector, from gy = dy * gamma, n = h * rstd and the row's mean c of
-// gy * n; stores dresidual and dx.
-template <typename T>
-__device__ __forceinline__ void back_vec(const NormBackArgs& a, uint32_t row, uint32_t c, int n, const float* gy,
-                                         const float* nh, float rstd, float mean) {
+// g of one vector, from its dh, gy = dy * gamma, n = h * rstd and the row's mean
+// of gy * n; stores dresidual and dx.
+template <typename T, bool STREAM>
+__device__ __forceinline__ void back_vec(const NormBackArgs& a, uint32_t row, uint32_t c, int n, u32x4_t dh,
+                                         const float* gy, const float* nh, float rstd, float mean) {
   constexpr int N = VecOf<T>::N;
   float g[N];
 #pragma unroll
   for (int i = 0; i < N; i++) g[i] = rstd * (gy[i] - nh[i] * mean);
   if (a.dh != nullptr) {
     float d[N];
-    VecOf<T>::unpack(load_vec(static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh + c, n), d);
+    VecOf<T>::unpack(dh, d);
 #pragma unroll
     for (int i = 0; i < N; i++) g[i] = d[i] + g[i];
   }
-  if (a.dr != nullptr) store_vec(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(g), n);
+  if (a.dr != nullptr) store_vec<T, STREAM>(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(g), n);
   if (a.dx != nullptr) {
     if (a.drop.cut != 0) drop<N>(g, row * a.cols + c, a.drop);
-    store_vec(static_cast<T*>(a.dx) + (int64_t)row * a.ld_dx + c, VecOf<T>::pack(g), n);
+    store_vec<T, STREAM>(static_cast<T*>(a.dx) + (int64_t)row * a.ld_dx + c, VecOf<T>::pack(g), n);
   }
 }
 
-// Rows of up to G * VPT vectors: each group of G lanes walks rows with a
-// stride, its dgamma sums in registers; the groups of a workgroup add theirs in
-// LDS in order, and the workgroup writes one row of partial sums.
-template <typename T, int G, int VPT>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_rms_norm_back(NormBackArgs a) {
+// Rows of up to G * VPT vectors: each group of G lanes walks rows with a stride,
+// its dgamma sums in registers (from VPT 3 on, where a group is the workgroup, in
+// LDS: the registers hold three tensors' vectors); the groups of a workgroup add
+// theirs in LDS (G VPT N floats) in order, and the workgroup writes one row of
+// partial sums.
+template <typename T, int VPT, bool STREAM>
+__global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
   constexpr int N = VecOf<T>::N;
-  constexpr int NT = G < 256 ? 256 : G;
-  constexpr int GROUPS = NT / G;
-  __shared__ float red[NT / 64];
-  __shared__ float comb[GROUPS > 1 ? G * VPT * N : 1];
-  const uint32_t grp = threadIdx.x / G, j = threadIdx.x % G;
-  float acc[VPT][N];
+  __shared__ float red[16];
+  extern __shared__ float comb[];
+  const int groups = blockDim.x / G;
+  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  constexpr bool IN_LDS = VPT >= 3;
+  float acc[IN_LDS ? 1 : VPT][N];
 #pragma unroll
   for (int k = 0; k < VPT; k++)
 #pragma unroll
-    for (int i = 0; i < N; i++) acc[k][i] = 0.0f;
-  for (uint32_t r0 = blockIdx.x * GROUPS; r0 < a.rows; r0 += gridDim.x * GROUPS) {
-    const uint32_t row = r0 + grp;
-    const bool live = row < a.rows;
-    const float rstd = live ? a.rstd[row] : 0.0f;
-    const T* dyr = static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy;
-    const T* hr = static_cast<const T*>(a.h) + (int64_t)row * a.ld_h;
-    u32x4_t vy[VPT], vh[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; k++) {
-      const uint32_t c = (j + k * G) * N;
-      const int n = live ? (int)a.cols - (int)c : 0;
-      vy[k] = vh[k] = u32x4_t{0, 0, 0, 0};
-      if (n > 0) {
-        vy[k] = load_vec(dyr + c, n);
-        vh[k] = load_vec(hr + c, n);
-      }
+    for (int i = 0; i < N; i++) {
+      if constexpr (IN_LDS)
+        comb[(j + k * G) * N + i] = 0.0f;
+      else
+        acc[k][i] = 0.0f;
     }
+  u32x4_t vy[VPT], vh[VPT], vd[VPT];
+  // vector k of a row (zeros past its end, or where there is no such row)
+  auto load = [&](int64_t row, int k) {
+    const uint32_t c = (j + k * G) * N;
+    const int n = row < a.rows ? (int)a.cols - (int)c : 0;
+    vy[k] = vh[k] = vd[k] = u32x4_t{0, 0, 0, 0};
+    if (n > 0) {
+      vy[k] = load_vec<T, STREAM>(static_cast<const T*>(a.dy) + row * a.ld_dy + c, n);
+      vh[k] = load_vec<T, STREAM>(static_cast<const T*>(a.h) + row * a.ld_h + c, n);
+      if (a.dh != nullptr) vd[k] = load_vec<T, STREAM>(static_cast<const T*>(a.dh) + row * a.ld_dh + c, n);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * groups;
+  const int64_t first = (int64_t)blockIdx.x * groups + grp;
+#pragma unroll
+  for (int k = 0; k < VPT; k++) load(first, k);
+  float next_rstd = first < a.rows ? a.rstd[first] : 0.0f;
+  for (int64_t row = first; row - grp < a.rows; row += step) {
+    const bool live = row < a.rows;
+    const float rstd = next_rstd;
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
       const int n = live ? (int)a.cols - (int)c : 0;
+      if (n <= 0) continue;
       float dy[N], nh[N], g[N];
       VecOf<T>::unpack(vy[k], dy);
       VecOf<T>::unpack(vh[k], nh);
-      if (n > 0) {
-        load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
+      load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
+      float* sums = IN_LDS ? comb + (j + k * G) * N : acc[IN_LDS ? 0 : k];
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-          nh[i] *= rstd;
-          s += (dy[i] * g[i]) * nh[i];
-          acc[k][i] += dy[i] * nh[i];
-        }
+      for (int i = 0; i < N; i++) {
+        nh[i] *= rstd;
+        s += (dy[i] * g[i]) * nh[i];
+        sums[i] += dy[i] * nh[i];
       }
     }
-    const float mean = group_sum<G>(s, red) / (float)a.cols;
-    if (a.dx == nullptr && a.dr == nullptr) continue;
+    const float mean = group_sum(s, G, red) / (float)a.cols;
+    next_rstd = row + step < a.rows ? a.rstd[row + step] : 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
       const int n = live ? (int)a.cols - (int)c : 0;
-      if (n <= 0) continue;
-      float gy[N], nh[N], g[N];
-      VecOf<T>::unpack(vy[k], gy);
-      VecOf<T>::unpack(vh[k], nh);
-      load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
+      if (n > 0 && (a.dx != nullptr || a.dr != nullptr)) {
+        float gy[N], nh[N], g[N];
+        VecOf<T>::unpack(vy[k], gy);
+        VecOf<T>::unpack(vh[k], nh);
+        load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        gy[i] *= g[i];
-        nh[i] *= rstd;
+        for (int i = 0; i < N; i++) {
+          gy[i] *= g[i];
+          nh[i] *= rstd;
+        }
+        back_vec<T, STREAM>(a, (uint32_t)row, c, n, vd[k], gy, nh, rstd, mean);
       }
-      back_vec<T>(a, row, c, n, gy, nh, rstd, mean);
+      load(row + step, k);  // the next row's, while this one's stores go out
     }
   }
   if (a.partial == nullptr) return;
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
-  if constexpr (GROUPS > 1) {
-#pragma unroll 1
-    for (int q = 0; q < GROUPS; q++) {
-      if ((int)grp == q) {
+  if constexpr (IN_LDS) {
+    __syncthreads();
+  } else if (groups == 1) {
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      const int64_t c = (int64_t)(j + k * G) * N;
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if (c + i < a.cols) out[c + i] = acc[k][i];
+    }
+    return;
+  } else {
+    for (int q = 0; q < groups; q++) {
+      if (grp == q) {
 #pragma unroll
         for (int k = 0; k < VPT; k++)
 #pragma unroll
@@ -383,16 +412,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_rms_norm_back(NormBackArg
       }
       __syncthreads();
     }
-    for (uint32_t c = threadIdx.x; c < a.cols; c += NT) out[c] = comb[c];
-  } else {
-#pragma unroll
-    for (int k = 0; k < VPT; k++) {
-      const int64_t c = (int64_t)(j + k * G) * N;
-#pragma unroll
-      for (int i = 0; i < N; i++)
-        if (c + i < a.cols) out[c + i] = acc[k][i];
-    }
   }
+  for (uint32_t c = threadIdx.x; c < a.cols; c += blockDim.x) out[c] = comb[c];
 }
 
 // Wider rows: dy and h are read twice, and the workgroup's dgamma sums stay in
@@ -421,7 +442,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back_wide(NormBackArgs a) {
       }
       s += t;
     }
-    const float mean = group_sum<1024>(s, red) / (float)a.cols;
+    const float mean = group_sum(s, 1024, red) / (float)a.cols;
     if (a.dx == nullptr && a.dr == nullptr) continue;
     for (int64_t c = (int64_t)threadIdx.x * N; c < a.cols; c += 1024 * N) {
       const int n = (int)min((int64_t)N, (int64_t)a.cols - c);
@@ -434,7 +455,9 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back_wide(NormBackArgs a) {
         gy[i] *= g[i];
         nh[i] *= rstd;
       }
-      back_vec<T>(a, row, (uint32_t)c, n, gy, nh, rstd, mean);
+      const u32x4_t dh = a.dh == nullptr ? u32x4_t{0, 0, 0, 0}
+                                         : load_vec(static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh + c, n);
+      back_vec<T, true>(a, row, (uint32_t)c, n, dh, gy, nh, rstd, mean);
     }
   }
 }
@@ -447,8 +470,10 @@ __global__ __launch_bounds__(256) void k_dgamma(const float* partial, uint32_t p
   const uint32_t c = blockIdx.x * 32 + lane;
   const uint32_t p0 = parts * slice / 8, p1 = parts * (slice + 1) / 8;
   float s = 0.0f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (uint32_t p = p0; p < p1; p++) s += partial[(int64_t)p * cols + c];
+  }
   part[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && c < cols) {
@@ -459,36 +484,37 @@ __global__ __launch_bounds__(256) void k_dgamma(const float* partial, uint32_t p
   }
 }
 
-// Workgroups of a backward pass, each with one row of partial sums.
-constexpr int64_t kBackGroups = 512;
+// A backward pass keeps about two workgroups of 640 lanes on each CU of a 256-CU
+// MI355X, or one of up to 1024 for wider rows: more of them write more partial
+// sums than their overlap gains (8192 x 5120: 92 us at 512 workgroups, 115 at 1024).
+constexpr int64_t kCus = 256;
+constexpr int kBackThreads = 640;
 
-// f(G, VPT) for rows of `vecs` vectors: the fewest lanes that hold a row with
-// at most four vectors each, up to 1024 lanes with eight.  Returns false for a
-// wider row.
-template <typename F>
-bool by_width(int64_t vecs, F&& f) {
-  using std::integral_constant;
-#define NVFP4_WIDTH(G, VPT)                                                \
-  if (vecs <= (G) * (VPT)) {                                               \
-    f(integral_constant<int, G>{}, integral_constant<int, VPT>{});         \
-    return true;                                                           \
+// Lanes and vectors per lane of a row of `vecs` vectors, with `want` vectors a lane
+// where up to 1024 lanes allow it; vpt 0 where the row is too wide.
+struct RowShape {
+  int G, vpt;
+};
+RowShape row_shape(int64_t vecs, int want) {
+  for (int vpt : {1, 2, 3, 5, 8}) {
+    if (vpt < want || vecs > 1024 * vpt) continue;
+    const int lanes = (int)((vecs + vpt - 1) / vpt);
+    return RowShape{lanes <= 16 ? 16 : lanes <= 32 ? 32 : (lanes + 63) / 64 * 64, vpt};
   }
-  NVFP4_WIDTH(16, 1)
-  NVFP4_WIDTH(32, 1)
-  NVFP4_WIDTH(64, 1)
-  NVFP4_WIDTH(64, 2)
-  NVFP4_WIDTH(256, 1)
-  NVFP4_WIDTH(256, 2)
-  NVFP4_WIDTH(256, 3)
-  NVFP4_WIDTH(512, 2)
-  NVFP4_WIDTH(512, 3)
-  NVFP4_WIDTH(512, 4)
-  NVFP4_WIDTH(1024, 3)
-  NVFP4_WIDTH(1024, 4)
-  NVFP4_WIDTH(1024, 5)
-  NVFP4_WIDTH(1024, 8)
-#undef NVFP4_WIDTH
-  return false;
+  return RowShape{0, 0};
+}
+
+// f(VPT) with the number of vectors as a constant
+template <typename F>
+void with_vpt(int vpt, F&& f) {
+  using std::integral_constant;
+  switch (vpt) {
+    case 1: f(integral_constant<int, 1>{}); break;
+    case 2: f(integral_constant<int, 2>{}); break;
+    case 3: f(integral_constant<int, 3>{}); break;
+    case 5: f(integral_constant<int, 5>{}); break;
+    default: f(integral_constant<int, 8>{});
+  }
 }
 
 template <typename T>
@@ -511,29 +537,78 @@ hipError_t dropout_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, vo
   return hipGetLastError();
 }
 
+// Bytes from which on a launch streams past the caches (256 MB hold little of it
+// until the next reader comes).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
+// Two vectors a lane stream best, one finishes a few rows soonest.
+constexpr int64_t kManyRows = 1024;
+
 template <typename T, bool MX>
 hipError_t norm_t(const NormArgs& a, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
   const int64_t vecs = ((int64_t)a.cols + N - 1) / N;
-  const bool held = by_width(vecs, [&](auto G, auto VPT) {
-    constexpr int g = G.value, v = VPT.value, nt = g < 256 ? 256 : g;
-    const uint32_t rpb = nt / g;
-    k_rms_norm<T, g, v, MX><<<(a.rows + rpb - 1) / rpb, nt, 0, s>>>(a);
+  const RowShape r = row_shape(vecs, a.rows >= kManyRows && vecs > 128 ? 2 : 1);
+  if (r.vpt == 0) {
+    k_rms_norm_wide<T, MX><<<a.rows, 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int rows = std::max(1, 256 / r.G);  // of a workgroup, where they are narrow
+  const int threads = r.G < 64 ? rows * r.G : r.G;
+  const unsigned grid = (a.rows + threads / r.G - 1) / (threads / r.G);
+  const bool stream = (int64_t)a.rows * a.cols * 4 * (int64_t)sizeof(T) >= kStreamBytes;
+  with_vpt(r.vpt, [&](auto vpt) {
+    if (stream)
+      k_rms_norm<T, vpt.value, MX, true><<<grid, threads, 0, s>>>(a, r.G);
+    else
+      k_rms_norm<T, vpt.value, MX, false><<<grid, threads, 0, s>>>(a, r.G);
   });
-  if (!held) k_rms_norm_wide<T, MX><<<a.rows, 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 
+// Shape of a backward pass of vectors of N elements: rows (groups of G lanes) per
+// workgroup, and workgroups, each with one row of partial sums.
+struct BackShape {
+  RowShape row;
+  int groups;
+  int64_t parts;
+};
+BackShape back_shape(int64_t rows, int64_t cols, int N) {
+  BackShape b;
+  b.row = row_shape((cols + N - 1) / N, 1);
+  if (b.row.vpt * N > 32) b.row = RowShape{0, 0};  // its sums do not fit in LDS
+  if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
+  b.groups = std::max(1, kBackThreads / b.row.G);
+  const int64_t most = b.row.G * b.groups <= kBackThreads ? 2 * kCus : kCus;
+  // few rows: two or more of them to each partial row
+  if (rows <= 2 * kCus && b.row.G <= 512) b.groups = std::max(b.groups, 2);
+  b.groups = (int)std::min<int64_t>(b.groups, rows);
+  b.parts = std::min((rows + b.groups - 1) / b.groups, most);
+  return b;
+}
+
 template <typename T>
-hipError_t norm_back_t(const NormBackArgs& a, int64_t parts, hipStream_t s) {
+hipError_t norm_back_t(const NormBackArgs& a, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
-  const int64_t vecs = ((int64_t)a.cols + N - 1) / N;
-  const bool held = by_width(vecs, [&](auto G, auto VPT) {
-    constexpr int g = G.value, v = VPT.value, nt = g < 256 ? 256 : g;
-    k_rms_norm_back<T, g, v><<<(unsigned)parts, nt, 0, s>>>(a);
+  const BackShape b = back_shape(a.rows, a.cols, N);
+  const RowShape r = b.row;
+  const int groups = b.groups;
+  const int64_t parts = b.parts;
+  if (r.vpt == 0) {
+    k_rms_norm_back_wide<T><<<(unsigned)parts, 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const bool stream = (int64_t)a.rows * a.cols * 5 * (int64_t)sizeof(T) >= kStreamBytes;
+  const int lds = groups == 1 && r.vpt < 3 ? 0 : r.G * r.vpt * N * (int)sizeof(float);
+  hipError_t e = hipSuccess;
+  with_vpt(r.vpt, [&](auto vpt) {
+    constexpr int VPT = vpt.value * N <= 32 ? vpt.value : 1;  // what back_shape picks
+    auto* kernel = stream ? &k_rms_norm_back<T, VPT, true> : &k_rms_norm_back<T, VPT, false>;
+    if (lds > 64 * 1024)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e == hipSuccess) kernel<<<(unsigned)parts, groups * r.G, lds, s>>>(a, r.G);
   });
-  if (!held) k_rms_norm_back_wide<T><<<(unsigned)parts, 1024, 0, s>>>(a);
-  return hipGetLastError();
+  return e == hipSuccess ? hipGetLastError() : e;
 }
 
 }  // namespace
@@ -555,21 +630,22 @@ hipError_t launch_rms_norm(const void* x, const void* residual, int dt, int64_t 
   return y == nullptr ? norm_t<float, true>(a, s) : norm_t<float, false>(a, s);
 }
 
-// A workgroup's partial row is worth its write where it sums several rows.
-static int64_t back_parts(int64_t rows) { return std::min(rows, kBackGroups); }
-
-int64_t rms_norm_back_workspace(int64_t rows, int64_t cols) { return back_parts(rows) * cols * (int64_t)sizeof(float); }
+int64_t rms_norm_back_workspace(int64_t rows, int64_t cols) {
+  if (rows == 0) return 0;
+  const int64_t parts = std::max(back_shape(rows, cols, 8).parts, back_shape(rows, cols, 4).parts);
+  return parts * cols * (int64_t)sizeof(float);
+}
 
 hipError_t launch_rms_norm_back(const void* dy, const void* dh, const void* h, int dt, int64_t rows, int64_t cols,
                                 int64_t ld_dy, int64_t ld_dh, int64_t ld_h, const void* gamma, int gamma_dt,
                                 const float* rstd, float p, uint64_t seed, void* dx, int64_t ld_dx, void* dresidual,
                                 int64_t ld_dr, float* dgamma, void* workspace, hipStream_t s) {
-  const int64_t parts = back_parts(rows);
+  const int64_t parts = rows == 0 ? 0 : back_shape(rows, cols, dt == 0 ? 8 : 4).parts;
   float* partial = dgamma == nullptr ? nullptr : static_cast<float*>(workspace);
   if (rows > 0) {
     NormBackArgs a{dy,   dh,    h,     gamma, rstd,           dx,             dresidual, partial,              ld_dy,
                    ld_dh, ld_h, ld_dx, ld_dr, (uint32_t)rows, (uint32_t)cols, gamma_dt,  make_dropout(p, seed)};
-    hipError_t e = dt == 0 ? norm_back_t<uint16_t>(a, parts, s) : norm_back_t<float>(a, parts, s);
+    hipError_t e = dt == 0 ? norm_back_t<uint16_t>(a, s) : norm_back_t<float>(a, s);
     if (e != hipSuccess) return e;
   }
   if (dgamma == nullptr) return hipSuccess;
