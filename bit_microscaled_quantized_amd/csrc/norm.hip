@@ -40,37 +40,38 @@ __device__ __forceinline__ float group_sum(float v, int G, float* red) {
 
 // ---- dropout
 
-// Rows are cut into segments of G * U vectors; a workgroup of 256 lanes takes
-// 256 / G segments of consecutive rows (G lanes each).
+// Rows are cut into equal segments of up to U vectors a lane.  Narrow rows share a
+// workgroup, 1 << lg lanes each (lg < 8); wider ones take a workgroup per segment.
 constexpr int DROP_U = 4;
 
-template <typename T>
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void k_dropout(const T* x, int64_t ld_x, T* y, int64_t ld_y, uint32_t rows,
-                                                 uint32_t cols, uint32_t segs, int lg, Dropout d) {
+                                                 uint32_t cols, uint32_t segs, uint32_t seg_vecs, int lg, Dropout d) {
   constexpr int N = VecOf<T>::N;
-  const uint32_t G = 1u << lg;
   const uint32_t rb = blockIdx.x / segs, seg = blockIdx.x - rb * segs;
-  const uint32_t row = rb * (256u >> lg) + (threadIdx.x >> lg);
+  const uint32_t lanes = lg < 8 ? 1u << lg : blockDim.x;
+  const uint32_t row = lg < 8 ? rb * (256u >> lg) + (threadIdx.x >> lg) : rb;
   if (row >= rows) return;
-  const uint32_t j = threadIdx.x & (G - 1);
+  const uint32_t j = lg < 8 ? threadIdx.x & (lanes - 1) : threadIdx.x;
   const T* xr = x + (int64_t)row * ld_x;
   T* yr = y + (int64_t)row * ld_y;
   u32x4_t v[DROP_U];
   int n[DROP_U];
 #pragma unroll
   for (int u = 0; u < DROP_U; u++) {
-    const int64_t c = ((int64_t)seg * DROP_U + u) * G * N + (int64_t)j * N;
-    n[u] = (int)min((int64_t)N, (int64_t)cols - c);
-    if (n[u] > 0) v[u] = load_vec(xr + c, n[u]);
+    const uint32_t at = j + u * lanes;  // vector of the segment
+    const int64_t c = ((int64_t)seg * seg_vecs + at) * N;
+    n[u] = at < seg_vecs ? (int)min((int64_t)N, (int64_t)cols - c) : 0;
+    if (n[u] > 0) v[u] = load_vec<T, STREAM>(xr + c, n[u]);
   }
 #pragma unroll
   for (int u = 0; u < DROP_U; u++) {
     if (n[u] <= 0) continue;
-    const uint32_t c = (seg * DROP_U + u) * G * N + j * N;
+    const uint32_t c = (seg * seg_vecs + j + u * lanes) * N;
     float f[N];
     VecOf<T>::unpack(v[u], f);
     drop<N>(f, row * cols + c, d);
-    store_vec(yr + c, VecOf<T>::pack(f), n[u]);
+    store_vec<T, STREAM>(yr + c, VecOf<T>::pack(f), n[u]);
   }
 }
 
@@ -305,8 +306,8 @@ __device__ __forceinline__ void back_vec(const NormBackArgs& a, uint32_t row, ui
 }
 
 // Rows of up to G * VPT vectors: each group of G lanes walks rows with a stride,
-// its dgamma sums in registers (from VPT 3 on, where a group is the workgroup, in
-// LDS: the registers hold three tensors' vectors); the groups of a workgroup add
+// its dgamma sums in registers (FP32 rows of five vectors a lane or more, where a
+// group is the workgroup, in LDS: the registers hold three tensors' vectors); the groups of a workgroup add
 // theirs in LDS (G VPT N floats) in order, and the workgroup writes one row of
 // partial sums.
 template <typename T, int VPT, bool STREAM>
@@ -316,7 +317,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
   extern __shared__ float comb[];
   const int groups = blockDim.x / G;
   const int grp = threadIdx.x / G, j = threadIdx.x % G;
-  constexpr bool IN_LDS = VPT >= 3;
+  constexpr bool IN_LDS = N == 4 && VPT >= 5;
   float acc[IN_LDS ? 1 : VPT][N];
 #pragma unroll
   for (int k = 0; k < VPT; k++)
@@ -327,26 +328,25 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
       else
         acc[k][i] = 0.0f;
     }
-  u32x4_t vy[VPT], vh[VPT], vd[VPT];
-  // vector k of a row (zeros past its end, or where there is no such row)
-  auto load = [&](int64_t row, int k) {
-    const uint32_t c = (j + k * G) * N;
-    const int n = row < a.rows ? (int)a.cols - (int)c : 0;
-    vy[k] = vh[k] = vd[k] = u32x4_t{0, 0, 0, 0};
-    if (n > 0) {
-      vy[k] = load_vec<T, STREAM>(static_cast<const T*>(a.dy) + row * a.ld_dy + c, n);
-      vh[k] = load_vec<T, STREAM>(static_cast<const T*>(a.h) + row * a.ld_h + c, n);
-      if (a.dh != nullptr) vd[k] = load_vec<T, STREAM>(static_cast<const T*>(a.dh) + row * a.ld_dh + c, n);
-    }
-  };
-  const int64_t step = (int64_t)gridDim.x * groups;
-  const int64_t first = (int64_t)blockIdx.x * groups + grp;
-#pragma unroll
-  for (int k = 0; k < VPT; k++) load(first, k);
-  float next_rstd = first < a.rows ? a.rstd[first] : 0.0f;
-  for (int64_t row = first; row - grp < a.rows; row += step) {
+  for (uint32_t r0 = blockIdx.x * groups; r0 < a.rows; r0 += gridDim.x * groups) {
+    const uint32_t row = r0 + grp;
     const bool live = row < a.rows;
-    const float rstd = next_rstd;
+    const float rstd = live ? a.rstd[row] : 0.0f;
+    const T* dyr = static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy;
+    const T* hr = static_cast<const T*>(a.h) + (int64_t)row * a.ld_h;
+    const T* dhr = static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh;
+    u32x4_t vy[VPT], vh[VPT], vd[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      const uint32_t c = (j + k * G) * N;
+      const int n = live ? (int)a.cols - (int)c : 0;
+      vy[k] = vh[k] = vd[k] = u32x4_t{0, 0, 0, 0};
+      if (n > 0) {
+        vy[k] = load_vec<T, STREAM>(dyr + c, n);
+        vh[k] = load_vec<T, STREAM>(hr + c, n);
+        if (a.dh != nullptr) vd[k] = load_vec<T, STREAM>(dhr + c, n);
+      }
+    }
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
@@ -366,24 +366,22 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
       }
     }
     const float mean = group_sum(s, G, red) / (float)a.cols;
-    next_rstd = row + step < a.rows ? a.rstd[row + step] : 0.0f;
+    if (a.dx == nullptr && a.dr == nullptr) continue;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
       const int n = live ? (int)a.cols - (int)c : 0;
-      if (n > 0 && (a.dx != nullptr || a.dr != nullptr)) {
-        float gy[N], nh[N], g[N];
-        VecOf<T>::unpack(vy[k], gy);
-        VecOf<T>::unpack(vh[k], nh);
-        load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
+      if (n <= 0) continue;
+      float gy[N], nh[N], g[N];
+      VecOf<T>::unpack(vy[k], gy);
+      VecOf<T>::unpack(vh[k], nh);
+      load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-          gy[i] *= g[i];
-          nh[i] *= rstd;
-        }
-        back_vec<T, STREAM>(a, (uint32_t)row, c, n, vd[k], gy, nh, rstd, mean);
+      for (int i = 0; i < N; i++) {
+        gy[i] *= g[i];
+        nh[i] *= rstd;
       }
-      load(row + step, k);  // the next row's, while this one's stores go out
+      back_vec<T, STREAM>(a, row, c, n, vd[k], gy, nh, rstd, mean);
     }
   }
   if (a.partial == nullptr) return;
@@ -517,6 +515,10 @@ void with_vpt(int vpt, F&& f) {
   }
 }
 
+// Bytes from which on a launch streams past the caches (256 MB hold little of it
+// until the next reader comes).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
 template <typename T>
 hipError_t dropout_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, void* y, int64_t ld_y, const Dropout& d,
                      hipStream_t s) {
@@ -529,17 +531,21 @@ hipError_t dropout_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, vo
   const int64_t vecs = (cols + N - 1) / N;
   int lg = 4;
   while (lg < 8 && (int64_t(1) << lg) < vecs) lg++;
-  const int64_t segs = (vecs + (DROP_U << lg) - 1) / (DROP_U << lg);
-  const int64_t rpb = 256 >> lg;
-  const int64_t grid = (rows + rpb - 1) / rpb * segs;
-  k_dropout<T><<<(unsigned)grid, 256, 0, s>>>(static_cast<const T*>(x), ld_x, static_cast<T*>(y), ld_y,
-                                              (uint32_t)rows, (uint32_t)cols, (uint32_t)segs, lg, d);
+  const int64_t segs = (vecs + 256 * DROP_U - 1) / (256 * DROP_U);
+  const int64_t seg_vecs = (vecs + segs - 1) / segs;
+  const int threads = lg < 8 ? 256 : (int)((seg_vecs + 64 * DROP_U - 1) / (64 * DROP_U) * 64);
+  const int64_t rpb = lg < 8 ? 256 >> lg : 1;
+  const unsigned grid = (unsigned)((rows + rpb - 1) / rpb * segs);
+  const T* xp = static_cast<const T*>(x);
+  T* yp = static_cast<T*>(y);
+  if (rows * cols * 2 * (int64_t)sizeof(T) >= kStreamBytes)
+    k_dropout<T, true><<<grid, threads, 0, s>>>(xp, ld_x, yp, ld_y, (uint32_t)rows, (uint32_t)cols, (uint32_t)segs,
+                                                (uint32_t)seg_vecs, lg, d);
+  else
+    k_dropout<T, false><<<grid, threads, 0, s>>>(xp, ld_x, yp, ld_y, (uint32_t)rows, (uint32_t)cols, (uint32_t)segs,
+                                                 (uint32_t)seg_vecs, lg, d);
   return hipGetLastError();
 }
-
-// Bytes from which on a launch streams past the caches (256 MB hold little of it
-// until the next reader comes).
-constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 // Two vectors a lane stream best, one finishes a few rows soonest.
 constexpr int64_t kManyRows = 1024;
@@ -575,8 +581,9 @@ struct BackShape {
 };
 BackShape back_shape(int64_t rows, int64_t cols, int N) {
   BackShape b;
-  b.row = row_shape((cols + N - 1) / N, 1);
-  if (b.row.vpt * N > 32) b.row = RowShape{0, 0};  // its sums do not fit in LDS
+  const int64_t vecs = (cols + N - 1) / N;
+  b.row = row_shape(vecs, vecs <= kBackThreads ? 1 : 2);
+  if (b.row.vpt * N > 32) b.row = RowShape{0, 0};  // beyond the registers
   if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
   b.groups = std::max(1, kBackThreads / b.row.G);
   const int64_t most = b.row.G * b.groups <= kBackThreads ? 2 * kCus : kCus;
@@ -599,7 +606,7 @@ hipError_t norm_back_t(const NormBackArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   const bool stream = (int64_t)a.rows * a.cols * 5 * (int64_t)sizeof(T) >= kStreamBytes;
-  const int lds = groups == 1 && r.vpt < 3 ? 0 : r.G * r.vpt * N * (int)sizeof(float);
+  const int lds = groups == 1 && !(N == 4 && r.vpt >= 5) ? 0 : r.G * r.vpt * N * (int)sizeof(float);
   hipError_t e = hipSuccess;
   with_vpt(r.vpt, [&](auto vpt) {
     constexpr int VPT = vpt.value * N <= 32 ? vpt.value : 1;  // what back_shape picks
