@@ -194,7 +194,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a, int G) {
     // elements past the row's end were loaded as zeros and stay zeros
     sum_vec<T>(a, vx[k], vr[k], row, (j + k * G) * N, h[k]);
 #pragma unroll
-    for (int i = 0; i < N; i++) sq += h[k][i] * h[k][i];
+    for (int i = 0; i < N; i++) sq = __builtin_fmaf(h[k][i], h[k][i], sq);
   }
   sq = group_sum(sq, G, red);
   const float rstd = 1.0f / sqrtf(sq / (float)a.cols + a.eps);
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_wide(NormArgs a) {
     sum_vec<T>(a, load_vec(xr + c, n), a.residual == nullptr ? u32x4_t{0, 0, 0, 0} : load_vec(rr + c, n), row,
                (uint32_t)c, h);
 #pragma unroll
-    for (int i = 0; i < N; i++) s += h[i] * h[i];
+    for (int i = 0; i < N; i++) s = __builtin_fmaf(h[i], h[i], s);
     sq += s;
   }
   sq = group_sum(sq, 1024, red);
@@ -290,14 +290,9 @@ __device__ __forceinline__ void back_vec(const NormBackArgs& a, uint32_t row, ui
                                          const float* gy, const float* nh, float rstd, float mean) {
   constexpr int N = VecOf<T>::N;
   float g[N];
+  VecOf<T>::unpack(dh, g);  // zeros without one
 #pragma unroll
-  for (int i = 0; i < N; i++) g[i] = rstd * (gy[i] - nh[i] * mean);
-  if (a.dh != nullptr) {
-    float d[N];
-    VecOf<T>::unpack(dh, d);
-#pragma unroll
-    for (int i = 0; i < N; i++) g[i] = d[i] + g[i];
-  }
+  for (int i = 0; i < N; i++) g[i] = __builtin_fmaf(rstd, __builtin_fmaf(-nh[i], mean, gy[i]), g[i]);
   if (a.dr != nullptr) store_vec<T, STREAM>(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(g), n);
   if (a.dx != nullptr) {
     if (a.drop.cut != 0) drop<N>(g, row * a.cols + c, a.drop);
@@ -361,8 +356,8 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
 #pragma unroll
       for (int i = 0; i < N; i++) {
         nh[i] *= rstd;
-        s += (dy[i] * g[i]) * nh[i];
-        sums[i] += dy[i] * nh[i];
+        s = __builtin_fmaf(dy[i] * g[i], nh[i], s);
+        sums[i] = __builtin_fmaf(dy[i], nh[i], sums[i]);
       }
     }
     const float mean = group_sum(s, G, red) / (float)a.cols;

@@ -1,0 +1,172 @@
+"""The autograd layer over the operators between the quantized layers, their use
+together, under graph capture and on two streams."""
+import os
+import sys
+
+import pytest
+
+from tests import gpuio
+
+pytestmark = pytest.mark.gpu
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+
+def plain_step(torch, x, r, gamma, w, labels, eps=1e-5):
+    """FP64 loss of norm and head, for autograd."""
+    h = r + x
+    y = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + eps) * gamma
+    z = y.reshape(-1, y.shape[-1]) @ w.t()
+    valid = (labels >= 0) & (labels < w.shape[0])
+    picked = z.gather(1, torch.where(valid, labels, 0).reshape(-1, 1))[:, 0]
+    loss = torch.where(valid.reshape(-1), torch.logsumexp(z, 1) - picked, 0.0)
+    return loss.sum() / valid.sum().clamp(min=1), h
+
+
+def test_gradients_through_norm_and_loss():
+    """x -> add_rms_norm -> linear_cross_entropy against FP64 autograd of the same
+    formulas.  y, d, dy and the gradients are each rounded to BF16 once (2^-8 of the
+    value): a dozen such roundings, added as norms, stay within 2^-5."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import add_rms_norm, linear_cross_entropy
+    g = torch.Generator(device="cuda").manual_seed(3)
+    B, S, H, V = 3, 50, 256, 777
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    leaves = [rnd(B, S, H).bfloat16(), rnd(B, S, H).bfloat16(), (1 + 0.2 * rnd(H)).bfloat16(),
+              (rnd(V, H) * 0.06).bfloat16()]
+    labels = torch.randint(V, (B, S), generator=g, device="cuda")
+    labels[0, ::3] = -100
+    mine = [t.clone().requires_grad_() for t in leaves]
+    h, y = add_rms_norm(mine[0], mine[1], mine[2])
+    loss = linear_cross_entropy(y, mine[3], labels) + h.float().square().mean() * 0.01
+    loss.backward()
+    ref = [t.double().requires_grad_() for t in leaves]
+    want, hr = plain_step(torch, *ref, labels)
+    want = want + hr.square().mean() * 0.01
+    want.backward()
+    assert abs(loss.item() - want.item()) <= 2.0 ** -8 * want.item()
+    for a, b in zip(mine, ref):
+        err = (a.grad.double() - b.grad).norm() / b.grad.norm()
+        assert err.item() <= 2.0 ** -5, err.item()
+
+
+def test_dropout_backward_repeats_the_mask():
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import add_rms_norm, dropout
+    x = torch.randn(7, 33, device="cuda", requires_grad=True)
+    y = dropout(x, 0.4, 5)
+    y.backward(torch.ones_like(y))
+    assert torch.equal(x.grad != 0, y != 0)
+    wide = torch.randn(5, 3, 64, device="cuda")[..., 5:38].requires_grad_()  # a slice of wider rows
+    h, _ = add_rms_norm(wide, None, torch.ones(33, device="cuda"), p=0.4, seed=9)
+    (g,) = torch.autograd.grad(h.sum(), wide)
+    assert g.shape == wide.shape and torch.equal(g != 0, h != 0)
+
+
+def test_only_what_is_needed_is_computed():
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import add_rms_norm, token_cross_entropy
+    x = torch.randn(4, 64, device="cuda").bfloat16()
+    gamma = torch.ones(64, device="cuda", requires_grad=True)
+    h, y = add_rms_norm(x, None, gamma)
+    y.sum().backward()
+    assert gamma.grad is not None
+    w = torch.randn(50, 64, device="cuda").bfloat16().requires_grad_()
+    token_cross_entropy(x, w, torch.zeros(4, dtype=torch.int64, device="cuda")).sum().backward()
+    assert w.grad is not None and w.grad.isfinite().all()
+
+
+def test_example_trains():
+    import train_ffn_head
+    losses, diff = train_ffn_head.train(steps=25, hidden=256, ffn=512, blocks=2, vocab=2048, tokens=1024, report=None)
+    assert losses[-1] < 0.7 * losses[0], losses
+    assert diff <= 2.0 ** -3  # half a step of E4M3 on both sides of a BF16 value, relative to the largest
+
+
+def _calls(torch, nv, b, seed):
+    """Every entry point once; BF16, H = 264, T = 130."""
+    T, V, H = b["T"], b["V"], b["H"]
+    bf = nv.NVFP4_BF16
+    nv.nvfp4_dropout(b["x"], bf, T, H, H, 0.2, seed, b["y0"], H)
+    nv.nvfp4_rms_norm(b["y0"], b["r"], bf, T, H, H, H, b["g"], bf, 1e-5, 0.1, seed + 1, b["h"], H, b["y"], H, None, None,
+                      b["rstd"])
+    nv.nvfp4_rms_norm(b["y0"], b["r"], bf, T, H, H, H, b["g"], bf, 1e-5, 0.0, 0, None, 0, None, 0, b["codes"],
+                      b["scales"], None)
+    nv.nvfp4_linear_cross_entropy(T, V, H, b["y"], H, b["w"], H, b["labels"], b["loss"], b["lse"], b["ws"])
+    nv.nvfp4_linear_cross_entropy_backward(T, V, H, b["y"], H, b["w"], H, b["labels"], b["lse"], b["dloss"], b["dy"], H,
+                                           b["dw"], bf, H, 0.0, b["ws"])
+    nv.nvfp4_rms_norm_backward(b["dy"], None, b["h"], bf, T, H, H, 0, H, b["g"], bf, b["rstd"], 0.1, seed + 1, b["dx"], H,
+                               b["dr"], H, b["dg"], b["wsn"])
+
+
+OUT = ("y0", "h", "y", "rstd", "codes", "scales", "loss", "lse", "dy", "dw", "dx", "dr", "dg")
+
+
+def _buffers(torch, nv, T=130, V=1000, H=264, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    e = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device="cuda")
+    labels = torch.randint(V, (T,), generator=g, device="cuda")
+    labels[::5] = -100
+    b = dict(T=T, V=V, H=H, x=rnd(T, H).bfloat16(), r=rnd(T, H).bfloat16(), g=(1 + 0.1 * rnd(H)).bfloat16(),
+             w=(rnd(V, H) * 0.05).bfloat16(), labels=labels, dloss=rnd(T) / T)
+    b.update(y0=e(T, H), h=e(T, H), y=e(T, H), rstd=e(T, t=torch.float32), codes=e(T, H, t=torch.uint8),
+             scales=e(T, (H + 31) // 32, t=torch.uint8), loss=e(T, t=torch.float32), lse=e(T, t=torch.float32),
+             dy=e(T, H), dw=e(V, H), dx=e(T, H), dr=e(T, H), dg=e(H, t=torch.float32),
+             ws=e(nv.nvfp4_linear_cross_entropy_workspace_size(T, V, H, True), t=torch.uint8),
+             wsn=e(nv.nvfp4_rms_norm_backward_workspace_size(T, H), t=torch.uint8))
+    return b
+
+
+def _same(torch, a, b, what):
+    for k in OUT:
+        assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), f"{what}: {k} differs"
+
+
+@pytest.mark.parametrize("T", [3, 130, 300])
+def test_captured_calls_replay_exactly(T):
+    """All entry points in one graph, replayed three times with eager calls and
+    overwritten outputs between: every replay gives the eager results' bytes."""
+    torch = gpuio.torch_cuda()
+    import bit_microscaled_quantized_amd as nv
+    eager, graph = _buffers(torch, nv, T), _buffers(torch, nv, T)
+    _calls(torch, nv, eager, 5)
+    want = {k: eager[k].clone() for k in OUT}
+    g = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(g, stream=stream):
+            _calls(torch, nv, graph, 5)
+    for rep in range(3):
+        for k in OUT + ("ws", "wsn"):
+            graph[k].view(torch.uint8).fill_(0x5A)
+        _calls(torch, nv, eager, 5)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        _same(torch, graph, want, f"replay {rep}")
+        _same(torch, eager, want, f"eager calls before replay {rep}")
+
+
+def test_two_streams_at_once():
+    """Two streams with their own buffers, interleaved: the results of one at a time."""
+    torch = gpuio.torch_cuda()
+    import bit_microscaled_quantized_amd as nv
+    one, two = _buffers(torch, nv, seed=1), _buffers(torch, nv, seed=2)
+    _calls(torch, nv, one, 7)
+    _calls(torch, nv, two, 8)
+    want = [{k: b[k].clone() for k in OUT} for b in (one, two)]
+    for b in (one, two):
+        for k in OUT:
+            b[k].view(torch.uint8).fill_(0x5A)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(10):
+        for s, b, seed in zip(streams, (one, two), (7, 8)):
+            with torch.cuda.stream(s):
+                _calls(torch, nv, b, seed)
+    torch.cuda.synchronize()
+    for b, w, name in zip((one, two), want, "ab"):
+        _same(torch, b, w, f"stream {name}")
