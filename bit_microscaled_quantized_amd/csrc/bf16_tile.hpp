@@ -74,6 +74,7 @@ struct TileOperand {
 template <int W, bool KMAJOR>
 struct TileFetch {
   uint32_t off[2 * W];
+  uint32_t row0;  // KMAJOR: offset of load 0's row of k, the rows of a load further on per load
   static __device__ __forceinline__ int row(int wave, int lane, int j) {  // K along rows
     return 8 * (2 * W * wave + j) + (lane >> 3);
   }
@@ -82,6 +83,7 @@ struct TileFetch {
   }
   // K along rows: the whole offset; KMAJOR: that of the columns
   __device__ __forceinline__ void init(const TileOperand& o, int wave, int lane) {
+    row0 = (uint32_t)krow(wave, lane, 0) * (o.ld * 2);
 #pragma unroll
     for (int j = 0; j < 2 * W; j++) {
       if constexpr (!KMAJOR) {
@@ -94,12 +96,13 @@ struct TileFetch {
     }
   }
   // load j of stage kt
-  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int lane, int j) const {
+  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int j) const {
     if constexpr (KMAJOR) kt = min(kt, (o.krows - 1) / TILE_K);
     const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
                           (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
     uint32_t v = off[j];
-    if constexpr (KMAJOR) v += (uint32_t)min(krow(wave, lane, j), o.krows - 1 - kt * TILE_K) * (o.ld * 2);
+    if constexpr (KMAJOR)  // its row of k, at most the operand's last
+      v += min(row0 + (uint32_t)(j * (8 / W)) * (o.ld * 2), (uint32_t)(o.krows - 1 - kt * TILE_K) * (o.ld * 2));
     asm volatile("" : "+v"(v));  // a 32-bit offset register beside the scalar base
     __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (2 * W * wave + j) * 1024), 16, 0, 0);
   }
@@ -192,8 +195,8 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
       } else {
 #pragma unroll
         for (int j = 0; j < 2 * W; j++) {
-          fa.issue(a, kt, lds, wave, lane, j);
-          fb.issue(b, kt, lds + OPERAND, wave, lane, j);
+          fa.issue(a, kt, lds, wave, j);
+          fb.issue(b, kt, lds + OPERAND, wave, j);
         }
       }
       __builtin_amdgcn_s_waitcnt(0);
@@ -249,9 +252,9 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
 #define TILE_LOAD(kt, st, x)                             \
   do {                                                   \
     if ((x) & 1)                                         \
-      fb.issue(b, kt, (st) + OPERAND, wave, lane, (x) >> 1);   \
+      fb.issue(b, kt, (st) + OPERAND, wave, (x) >> 1);   \
     else                                                 \
-      fa.issue(a, kt, st, wave, lane, (x) >> 1);               \
+      fa.issue(a, kt, st, wave, (x) >> 1);               \
   } while (0)
   // fragments q in use; the next step's from step rs of rst; loads x0 .. x0 + 2 W - 1 of stage kt into dst
 #define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                      \
@@ -342,8 +345,8 @@ __device__ __forceinline__ void tile_product_short(const TileOperand& a, const T
     if (k > 0) __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2 * W; j++) {
-      fa.issue(a, k, lds, wave, lane, j);
-      fb.issue(b, k, lds + tile_operand(W), wave, lane, j);
+      fa.issue(a, k, lds, wave, j);
+      fb.issue(b, k, lds + tile_operand(W), wave, j);
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();

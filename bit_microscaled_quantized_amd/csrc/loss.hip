@@ -148,6 +148,51 @@ __global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, int64_t 
   if (tid == 1023) *tk.n = sums[1023];
 }
 
+// Both of the above for up to FEW_LABELS tokens, one launch: every workgroup
+// counts the labels itself (those before its 8 tokens, and all of them).
+constexpr int64_t FEW_LABELS = 2048;
+__global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, int T, int64_t V, const uint16_t* x,
+                                                       int64_t ld_x, int64_t H, Tokens tk, uint16_t* xc) {
+  __shared__ int part[2][4];
+  const int tid = threadIdx.x, first = blockIdx.x * 8;
+  auto labelled = [&](int t) { return t < T && labels[t] >= 0 && labels[t] < V; };
+  int before = 0, all = 0;
+  for (int t = tid; t < T; t += 256) {
+    const int v = labelled(t) ? 1 : 0;
+    all += v;
+    before += t < first ? v : 0;
+  }
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    all += __shfl_xor(all, m, 64);
+    before += __shfl_xor(before, m, 64);
+  }
+  if ((tid & 63) == 0) {
+    part[0][tid >> 6] = before;
+    part[1][tid >> 6] = all;
+  }
+  __syncthreads();
+  int at = part[0][0] + part[0][1] + part[0][2] + part[0][3];
+  const int n = part[1][0] + part[1][1] + part[1][2] + part[1][3];
+  if (blockIdx.x == 0 && tid == 0) *tk.n = n;
+  for (int t = first; t < first + 8; t++) {
+    const bool valid = labelled(t);
+    if (tid == 0 && t < T) {
+      tk.place[t] = valid ? at : -1;
+      if (valid) tk.list[at] = t;
+    }
+    if (valid) {
+      for (int64_t c = tid * 8; c < H; c += 256 * 8)
+        *reinterpret_cast<u32x4_t*>(xc + at * H + c) = *reinterpret_cast<const u32x4_t*>(x + t * ld_x + c);
+      at++;
+    }
+    // the grid covers T up to a multiple of 128: its rows past n are zeros where K needs them
+    if (t >= n && t < (n + 127) / 128 * 128)
+      for (int64_t c = tid * 8; c < H; c += 256 * 8)
+        *reinterpret_cast<u32x4_t*>(xc + t * H + c) = u32x4_t{0, 0, 0, 0};
+  }
+}
+
 // xc[i] = x[list[i]] for the n labelled tokens (nothing else of x is read
 // again), then zeros up to a multiple of 128 rows (K of the dw product).
 __global__ __launch_bounds__(256) void k_gather(const uint16_t* x, int64_t ld_x, int64_t H, Tokens tk, uint16_t* xc) {
@@ -475,7 +520,9 @@ DxPlan dx_plan(int64_t T, int64_t H, int64_t piece) {
     const int64_t slots = W == 4 ? 256 : 512, tiles = tiles_of(T, W) * tiles_of(H, W);
     for (int64_t r = 1; r <= 4 || r * slots < 2 * tiles + slots; r++) {
       const int64_t parts = std::max<int64_t>(1, std::min(r * slots / tiles, stages / 4));
-      const double us = round_us(tiles * parts, (double)stages / parts, W);
+      // the products, and the parts' FP32 sums, written and read at 4.5 TB/s
+      const double us = round_us(tiles * parts, (double)stages / parts, W) +
+                        (double)(parts * tiles_of(T, W) * tile_side(W) * H) * 8.0 / 4.5e6;
       if (us < best_us * 0.97) {
         best_us = us;
         best = DxPlan{W, std::max(r * slots, tiles)};
@@ -586,9 +633,14 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
   float* sum = reinterpret_cast<float*>(ws + pl.sum);
   int* tok = reinterpret_cast<int*>(ws + pl.tok);
   const Tokens tk{tok, tok + 1, tok + 1 + T};
-  k_tokens<<<1, 1024, 0, s>>>(labels, T, V, tk);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  k_gather<<<(unsigned)up128(T), 256, 0, s>>>(static_cast<const uint16_t*>(x), ld_x, H, tk, xc);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  if (T <= FEW_LABELS) {
+    k_tokens_gather<<<(unsigned)(up128(T) / 8), 256, 0, s>>>(labels, (int)T, V, xp, ld_x, H, tk, xc);
+  } else {
+    k_tokens<<<1, 1024, 0, s>>>(labels, T, V, tk);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    k_gather<<<(unsigned)up128(T), 256, 0, s>>>(xp, ld_x, H, tk, xc);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
     const int64_t n = std::min(pl.piece, V - v0);
