@@ -101,8 +101,9 @@ struct TileFetch {
     const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
                           (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
     uint32_t v = off[j];
-    if constexpr (KMAJOR)  // its row of k, at most the operand's last
-      v += min(row0 + (uint32_t)(j * (8 / W)) * (o.ld * 2), (uint32_t)(o.krows - 1 - kt * TILE_K) * (o.ld * 2));
+    if constexpr (KMAJOR)  // its row of k, at most the operand's last (64 rows stay within 32 bits, all need not)
+      v += min(row0 + (uint32_t)(j * (8 / W)) * (o.ld * 2),
+               (uint32_t)min(o.krows - 1 - kt * TILE_K, TILE_K) * (o.ld * 2));
     asm volatile("" : "+v"(v));  // a 32-bit offset register beside the scalar base
     __builtin_amdgcn_global_load_lds((tile_gvoid*)(base + v), (tile_lvoid*)(st + (2 * W * wave + j) * 1024), 16, 0, 0);
   }

@@ -155,6 +155,17 @@ def test_large_vocabularies_and_many_tokens(T, V, H):
     q.check_dw(dw, F32)
 
 
+def test_weight_rows_that_span_more_than_32_bits():
+    """Vocabulary rows 2 MiB apart: from one piece's first row to its last is more than
+    4 GiB, and some stages of the dx product end a few rows past that."""
+    q = Head(3, 2300, 64, 0.0, pad=(1 << 20) - 64, seed=11).reference()
+    loss, lse = q.forward()
+    q.check_forward(loss, lse)
+    dx, dw = q.backward(lse)
+    q.check_dx(dx)
+    q.check_dw(dw, BF)
+
+
 @pytest.mark.parametrize("T", [1, 20, 90, 300])
 @pytest.mark.parametrize("dw_dt", [BF, F32])
 def test_accumulated_weight_gradient_and_single_outputs(T, dw_dt):
