@@ -14,8 +14,8 @@ bool drop_ok(float p) { return p >= 0.0f && p < 1.0f - 0x1p-17f; }
 
 nvfp4_status check_rows(int64_t rows, int64_t cols) {
   if (rows < 0 || cols <= 0) return NVFP4_ESHAPE;
-  // element indices fit 32 bits, and so does the number of lanes a launch takes
-  if (rows >= (int64_t(1) << 28) || (rows > 0 && cols > ((int64_t(1) << 32) - 1) / rows)) return NVFP4_ESHAPE;
+  // element indices fit 32 bits, and so does the number of lanes a launch takes (16 a row or more)
+  if (rows > (int64_t(1) << 28) - 16 || (rows > 0 && cols > ((int64_t(1) << 32) - 1) / rows)) return NVFP4_ESHAPE;
   if (cols >= (int64_t(1) << 32)) return NVFP4_ESHAPE;
   return NVFP4_OK;
 }
@@ -123,6 +123,8 @@ nvfp4_status nvfp4_linear_cross_entropy_workspace_size(int64_t T, int64_t V, int
   if (T < 0 || T >= (int64_t(1) << 22) || V <= 0 || H <= 0 || V >= (int64_t(1) << 24) || H >= kMaxLd ||
       H % 8 != 0)
     return NVFP4_ESHAPE;
+  // the lanes of a launch (256 for 128 x 128 logits or more) fit 32 bits
+  if (T > (int64_t(1) << 37) / V) return NVFP4_ESHAPE;
   *bytes = T == 0 ? 0 : nvfp4::linear_ce_workspace(T, V, H, train != 0);
   return NVFP4_OK;
 }

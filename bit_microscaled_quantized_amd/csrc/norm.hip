@@ -460,20 +460,23 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back_wide(NormBackArgs a) {
 __global__ __launch_bounds__(256) void k_dgamma(const float* partial, uint32_t parts, uint32_t cols, float* dgamma) {
   __shared__ float part[8][32];
   const uint32_t lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const uint32_t c = blockIdx.x * 32 + lane;
   const uint32_t p0 = parts * slice / 8, p1 = parts * (slice + 1) / 8;
-  float s = 0.0f;
-  if (c < cols) {
+  for (uint64_t base = blockIdx.x * 32; base < cols; base += (uint64_t)gridDim.x * 32) {
+    const uint64_t c = base + lane;
+    float s = 0.0f;
+    if (c < cols) {
 #pragma unroll 8
-    for (uint32_t p = p0; p < p1; p++) s += partial[(int64_t)p * cols + c];
-  }
-  part[slice][lane] = s;
-  __syncthreads();
-  if (slice == 0 && c < cols) {
-    s = 0.0f;
+      for (uint32_t p = p0; p < p1; p++) s += partial[(int64_t)p * cols + c];
+    }
+    __syncthreads();  // the last columns' sums are read
+    part[slice][lane] = s;
+    __syncthreads();
+    if (slice == 0 && c < cols) {
+      s = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 8; q++) s += part[q][lane];
-    dgamma[c] = s;
+      for (int q = 0; q < 8; q++) s += part[q][lane];
+      dgamma[c] = s;
+    }
   }
 }
 
@@ -651,7 +654,8 @@ hipError_t launch_rms_norm_back(const void* dy, const void* dh, const void* h, i
     if (e != hipSuccess) return e;
   }
   if (dgamma == nullptr) return hipSuccess;
-  k_dgamma<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(partial, (uint32_t)parts, (uint32_t)cols, dgamma);
+  const unsigned grid = (unsigned)std::min<int64_t>((cols + 31) / 32, 1 << 20);  // lanes of a launch fit 32 bits
+  k_dgamma<<<grid, 256, 0, s>>>(partial, (uint32_t)parts, (uint32_t)cols, dgamma);
   return hipGetLastError();
 }
 

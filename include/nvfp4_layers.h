@@ -13,6 +13,7 @@
  *   - any column count and any leading dimension ld >= cols (in elements) is
  *     taken, and tensor pointers need only their element's alignment (16 bytes
  *     for the operands of the cross entropy, whose ld are multiples of 8);
+ *   - there are at most 2^28 - 16 rows;
  *   - zero rows (tokens) are no error: the call does nothing to per-row outputs
  *     (their pointers may be NULL), and sums over the rows are zero;
  *   - infinities and NaN are carried through as IEEE arithmetic carries them.
@@ -101,7 +102,7 @@ nvfp4_status nvfp4_rms_norm_backward_workspace_size(int64_t rows, int64_t cols, 
  * tiles and never stored.
  *   x [T][ld_x], w [V][ld_w] BF16, 16-byte aligned, ld a multiple of 8;
  *   labels [T] int64; loss, lse [T] FP32.  H a positive multiple of 8, V >= 1,
- *   T, H and every ld < 2^22, V < 2^24.
+ *   T, H and every ld < 2^22, V < 2^24, T * V <= 2^37.
  *   workspace: at least nvfp4_linear_cross_entropy_workspace_size(T, V, H, 0)
  *   bytes, 16-byte aligned, in use until the call's work on `stream` completes.
  *   Fewer bytes: NVFP4_ESHAPE.

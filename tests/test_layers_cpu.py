@@ -33,6 +33,7 @@ def dropout(**kw):
     (dict(ld_y=39), b.NVFP4_ESHAPE),
     (dict(ld_y=1 << 60), b.NVFP4_ESHAPE),
     (dict(rows=1 << 28, cols=1, ld_x=1, ld_y=1), b.NVFP4_ESHAPE),
+    (dict(rows=(1 << 28) - 15, cols=1, ld_x=1, ld_y=1), b.NVFP4_ESHAPE),  # 2^32 lanes
     (dict(rows=1 << 20, cols=1 << 12, ld_x=1 << 12, ld_y=1 << 12), b.NVFP4_ESHAPE),  # 2^32 elements
     (dict(x=FAKE + 1), b.NVFP4_EALIGN),
     (dict(dt=1, y=FAKE + 2), b.NVFP4_EALIGN),
@@ -144,6 +145,7 @@ def loss(**kw):
     (dict(H=60, ld_x=64, ld_w=64), b.NVFP4_ESHAPE),     # H must be a multiple of 8
     (dict(T=1 << 22), b.NVFP4_ESHAPE),
     (dict(V=1 << 24), b.NVFP4_ESHAPE),
+    (dict(T=1 << 20, V=(1 << 17) + 1, workspace_bytes=1 << 60), b.NVFP4_ESHAPE),
     (dict(ld_x=56), b.NVFP4_ESHAPE),
     (dict(ld_w=56), b.NVFP4_ESHAPE),
     (dict(ld_x=68), b.NVFP4_EALIGN),
@@ -208,3 +210,18 @@ def test_errors_raise_in_checked_mode():
     with pytest.raises(nv.Nvfp4Error) as e:
         nv.nvfp4_dropout(FAKE, 0, 4, 40, 40, 2.0, 0, FAKE, 40, stream=0)
     assert e.value.status == b.NVFP4_EINVAL
+
+
+def test_autograd_layer_refuses_host_tensors_and_wrong_shapes():
+    import torch
+    from bit_microscaled_quantized_amd import layers
+    x, w, y = torch.ones(4, 64).bfloat16(), torch.ones(10, 64).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    g = torch.ones(64).bfloat16()
+    with pytest.raises(ValueError, match="GPU"):
+        layers.dropout(x, 0.1, 1)
+    with pytest.raises(ValueError, match="GPU"):
+        layers.add_rms_norm(x, x, g)
+    with pytest.raises(ValueError, match="GPU"):
+        layers.rms_norm_mx8(x, x, g)
+    with pytest.raises(ValueError, match="GPU"):
+        layers.linear_cross_entropy(x, w, y)
