@@ -16,6 +16,7 @@ current stream, with buffers from its caching allocator.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import nvfp4 as nv
 
@@ -26,6 +27,29 @@ def _dt(t) -> int:
     if t.dtype not in _DT:
         raise TypeError(f"expected a bfloat16 or float32 tensor, got {t.dtype}")
     return _DT[t.dtype]
+
+
+def _on_gpu(x, *others):
+    """Refuses host tensors, and tensors on another device than x's: the kernels take
+    addresses."""
+    if not x.is_cuda:
+        raise ValueError(f"expected tensors on the GPU, got one on {x.device}")
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"expected tensors on {x.device}, got one on {t.device}")
+
+
+def _norm_args(x, residual, gamma):
+    """x and residual as matrices with their leading dimensions, and gamma packed."""
+    _on_gpu(x, residual, gamma)
+    if x.dim() == 0 or gamma.shape != x.shape[-1:]:
+        raise ValueError(f"gamma must have the shape of x's last dimension, got {tuple(gamma.shape)} for "
+                         f"{tuple(x.shape)}")
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError("residual must have x's shape and type")
+    m, ld = _rows(x)
+    r, ld_r = (None, 0) if residual is None else _rows(residual)
+    return m, ld, r, ld_r, gamma.contiguous()
 
 
 def _rows(t):
@@ -44,15 +68,17 @@ class _Dropout(torch.autograd.Function):
         return _run_dropout(x, p, seed)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         return _run_dropout(dy, ctx.p, ctx.seed), None, None
 
 
 def _run_dropout(x, p, seed):
+    _on_gpu(x)
     m, ld = _rows(x)
-    y = torch.empty(m.shape, dtype=m.dtype, device=m.device)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     nv.nvfp4_dropout(m, _dt(m), m.shape[0], m.shape[1], ld, p, seed, y, m.shape[1])
-    return y.view(x.shape)
+    return y
 
 
 def dropout(x, p: float, seed: int):
@@ -64,27 +90,26 @@ def dropout(x, p: float, seed: int):
 class _AddRmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, gamma, eps, p, seed):
-        m, ld = _rows(x)
+        m, ld, r, ld_r, g = _norm_args(x, residual, gamma)
         rows, cols = m.shape
         dt = _dt(m)
-        r, ld_r = (None, 0) if residual is None else _rows(residual)
-        if r is not None and (r.shape != m.shape or r.dtype != m.dtype):
-            raise ValueError("residual must have x's shape and type")
-        g = gamma.contiguous()
-        if g.shape != (cols,):
-            raise ValueError(f"gamma must have shape ({cols},), got {tuple(g.shape)}")
-        h, y = torch.empty((2, rows, cols), dtype=m.dtype, device=m.device)
+        # tensors of their own: y may be changed in place, and freed, while h is kept
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = torch.empty_like(h)
         rstd = torch.empty(rows, dtype=torch.float32, device=m.device)
         nv.nvfp4_rms_norm(m, r, dt, rows, cols, ld, ld_r, g, _dt(g), eps, p, seed, h, cols, y, cols, None, None, rstd)
+        ctx.set_materialize_grads(False)  # an unused h has no gradient to read
         ctx.save_for_backward(h, rstd, g)
-        ctx.meta = (x.shape, residual is not None, p, seed, gamma.dtype)
-        return h.view(x.shape), y.view(x.shape)
+        ctx.meta = (rows, cols, residual is not None, p, seed, gamma.dtype)
+        return h, y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh, dy):
         h, rstd, g = ctx.saved_tensors
-        shape, has_residual, p, seed, gamma_dtype = ctx.meta
-        rows, cols = h.shape
+        rows, cols, has_residual, p, seed, gamma_dtype = ctx.meta
+        if dy is None and dh is None:
+            return (None,) * 6
         dy, ld_dy = _rows(torch.zeros_like(h) if dy is None else dy)
         dh, ld_dh = (None, 0) if dh is None else _rows(dh)
         need_x, need_r, need_g = ctx.needs_input_grad[:3]
@@ -101,8 +126,7 @@ class _AddRmsNorm(torch.autograd.Function):
             ws = torch.empty(nv.nvfp4_rms_norm_backward_workspace_size(rows, cols), dtype=torch.uint8, device=h.device)
         nv.nvfp4_rms_norm_backward(dy, dh, h, _dt(h), rows, cols, ld_dy, ld_dh, cols, g, _dt(g), rstd, p, seed, dx,
                                    cols, dr, cols, dg, ws)
-        return (None if dx is None else dx.view(shape), None if dr is None else dr.view(shape),
-                None if dg is None else dg.to(gamma_dtype), None, None, None)
+        return dx, dr, None if dg is None else dg.to(gamma_dtype), None, None, None
 
 
 def add_rms_norm(x, residual, gamma, eps: float = 1e-5, p: float = 0.0, seed: int = 0):
@@ -114,17 +138,15 @@ def add_rms_norm(x, residual, gamma, eps: float = 1e-5, p: float = 0.0, seed: in
 def rms_norm_mx8(x, residual, gamma, eps: float = 1e-5):
     """(h, codes, scales): the norm's output as E4M3 codes with one UE8M0 scale per 32
     columns (torch.float8_e4m3fn and torch.float8_e8m0fnu); no gradient."""
-    m, ld = _rows(x)
+    m, ld, r, ld_r, g = _norm_args(x, residual, gamma)
     rows, cols = m.shape
-    r, ld_r = (None, 0) if residual is None else _rows(residual)
-    g = gamma.contiguous()
-    h = torch.empty((rows, cols), dtype=m.dtype, device=m.device)
+    h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=m.device)
     scales = torch.empty((rows, (cols + 31) // 32), dtype=torch.float8_e8m0fnu, device=m.device)
     nv.nvfp4_rms_norm(m, r, _dt(m), rows, cols, ld, ld_r, g, _dt(g), float(eps), 0.0, 0, h, cols, None, 0, codes, scales,
                       None)
     lead = x.shape[:-1]
-    return h.view(x.shape), codes.view(*lead, cols), scales.view(*lead, -1)
+    return h, codes.view(*lead, cols), scales.view(*lead, -1)
 
 
 class _LinearCrossEntropy(torch.autograd.Function):
@@ -132,11 +154,14 @@ class _LinearCrossEntropy(torch.autograd.Function):
     def forward(ctx, x, w, labels):
         if x.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
             raise TypeError("linear_cross_entropy takes bfloat16 hidden states and weight")
+        _on_gpu(x, w, labels)
+        if w.dim() != 2 or x.shape[-1:] != w.shape[1:] or labels.numel() * w.shape[1] != x.numel():
+            raise ValueError("expected x [..., H], weight [V, H] and one label per token")
+        if labels.is_floating_point() or labels.is_complex():
+            raise TypeError(f"expected integer labels, got {labels.dtype}")
         m, ld = _rows(x)
         T, H = m.shape
         V = w.shape[0]
-        if w.shape != (V, H) or labels.numel() != T:
-            raise ValueError("expected x [..., H], weight [V, H] and one label per token")
         # 16-byte rows: slices that break them are copied
         if ld % 8 or m.data_ptr() % 16:
             m, ld = m.contiguous(), H
@@ -154,6 +179,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         return loss.view(labels.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss):
         m, w, y, lse = ctx.saved_tensors
         T, V, H, ld, ld_w, shape = ctx.meta

@@ -76,6 +76,48 @@ def test_only_what_is_needed_is_computed():
     assert w.grad is not None and w.grad.isfinite().all()
 
 
+def test_arguments_of_the_autograd_layer():
+    """What does not fit is refused before any kernel runs, host tensors beside device ones too."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd import layers
+    x = torch.ones(4, 64, device="cuda").bfloat16()
+    g, w = torch.ones(64, device="cuda"), torch.ones(10, 64, device="cuda").bfloat16()
+    y = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for norm in (layers.add_rms_norm, layers.rms_norm_mx8):
+        for r, gain in ((x[:3], g), (x.float(), g), (x, g[:32]), (x, g[None]), (x.cpu(), g), (x, g.cpu())):
+            with pytest.raises(ValueError):
+                norm(x, r, gain)
+        with pytest.raises(TypeError):
+            norm(x.half(), None, g)
+    for args in ((x, w[:, :32], y), (x, w, y[:3]), (x, w, y.cpu()), (x, w.cpu(), y), (x, w[0], y)):
+        with pytest.raises(ValueError):
+            layers.token_cross_entropy(*args)
+    for args in ((x.float(), w, y), (x, w.float(), y), (x, w, y.float())):
+        with pytest.raises(TypeError):
+            layers.token_cross_entropy(*args)
+    with pytest.raises(TypeError):
+        layers.dropout(y, 0.1, 1)
+
+
+def test_outputs_may_be_changed_in_place():
+    """y may be, since only h is kept for the gradient; a change of h is reported."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import add_rms_norm
+    x = torch.randn(3, 5, 96, device="cuda", requires_grad=True)
+    gamma = torch.ones(96, device="cuda", requires_grad=True)
+    h, y = add_rms_norm(x, None, gamma)
+    (y * 2.0).sum().backward()
+    want = x.grad.clone()
+    x.grad = None
+    h, y = add_rms_norm(x, None, gamma)
+    y.mul_(2.0).sum().backward()
+    assert torch.equal(x.grad, want) and torch.isfinite(want).all()
+    h, y = add_rms_norm(x, None, gamma)
+    h.mul_(2.0)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+
+
 def test_example_trains():
     import train_ffn_head
     losses, diff = train_ffn_head.train(steps=25, hidden=256, ffn=512, blocks=2, vocab=2048, tokens=1024, report=None)
