@@ -21,19 +21,43 @@ namespace {
 
 constexpr int MXB = 32;  // columns per block of the 8-bit output
 
-// Sum over the G lanes of a group (inside a wave, or through the group's G / 64
-// places in red, one per wave of the workgroup); every lane gets the result.  All
+// v of another lane of its 16: DPP control CTRL
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over the aligned 16, 32 or 64 lanes of a span, a butterfly in the registers:
+// neighbours, pairs, quads (half mirrored), halves of 16 (mirrored), rows of 16,
+// halves of the wave.  (Through LDS, shuffle by shuffle, a sum over a wave takes
+// some 500 cycles, a tenth of what a row of 5120 takes in all.)
+__device__ __forceinline__ float span_sum(float v, int span) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  if (span > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (span > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+// Sum over the G lanes of a group: inside a wave, or through the group's G / 64
+// places in red, one per wave of the workgroup; every lane gets the result.  All
 // lanes of the workgroup call it together.
 __device__ __forceinline__ float group_sum(float v, int G, float* red) {
-  const int span = min(G, 64);
-  for (int m = 1; m < span; m <<= 1) v += __shfl_xor(v, m, 64);
+  v = span_sum(v, G);
   if (G > 64) {
     __syncthreads();  // the last use of red is over
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    const int waves = G / 64, first = (int)threadIdx.x / G * waves;
-    v = 0.0f;
-    for (int w = 0; w < waves; w++) v += red[first + w];
+    const int waves = G / 64, first = (int)threadIdx.x / G * waves, w = threadIdx.x & 15;
+    v = span_sum(w >= first && w < first + waves ? red[w] : 0.0f, 16);
   }
   return v;
 }
@@ -283,100 +307,158 @@ struct NormBackArgs {
   Dropout drop;
 };
 
-// g of one vector, from its dh, gy = dy * gamma, n = h * rstd and the row's mean
-// of gy * n; stores dresidual and dx.
-template <typename T, bool STREAM>
-__device__ __forceinline__ void back_vec(const NormBackArgs& a, uint32_t row, uint32_t c, int n, u32x4_t dh,
-                                         const float* gy, const float* nh, float rstd, float mean) {
-  constexpr int N = VecOf<T>::N;
-  float g[N];
-  VecOf<T>::unpack(dh, g);  // zeros without one
+// g of one vector: in, dh; out, dh + rstd * (dy * gamma - n * mean), n = h * rstd.
+template <int N>
+__device__ __forceinline__ void back_vec(float* g, const float* dy, const float* h, const float* gamma, float rstd,
+                                         float mean) {
 #pragma unroll
-  for (int i = 0; i < N; i++) g[i] = __builtin_fmaf(rstd, __builtin_fmaf(-nh[i], mean, gy[i]), g[i]);
+  for (int i = 0; i < N; i++)
+    g[i] = __builtin_fmaf(rstd, __builtin_fmaf(-(h[i] * rstd), mean, dy[i] * gamma[i]), g[i]);
+}
+
+// Stores dresidual and dx of one vector.
+template <typename T, bool STREAM>
+__device__ __forceinline__ void back_store(const NormBackArgs& a, uint32_t row, uint32_t c, int n, float* g) {
   if (a.dr != nullptr) store_vec<T, STREAM>(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(g), n);
   if (a.dx != nullptr) {
-    if (a.drop.cut != 0) drop<N>(g, row * a.cols + c, a.drop);
+    if (a.drop.cut != 0) drop<VecOf<T>::N>(g, row * a.cols + c, a.drop);
     store_vec<T, STREAM>(static_cast<T*>(a.dx) + (int64_t)row * a.ld_dx + c, VecOf<T>::pack(g), n);
   }
 }
 
+// A lane's vectors of a row: dy, h and dh.
+template <int VPT>
+struct BackRow {
+  u32x4_t dy[VPT], h[VPT], dh[VPT];
+  float rstd;
+};
+
 // Rows of up to G * VPT vectors: each group of G lanes walks rows with a stride,
 // its dgamma sums in registers (FP32 rows of five vectors a lane or more, where a
-// group is the workgroup, in LDS: the registers hold three tensors' vectors); the groups of a workgroup add
-// theirs in LDS (G VPT N floats) in order, and the workgroup writes one row of
-// partial sums.
-template <typename T, int VPT, bool STREAM>
-__global__ __launch_bounds__(1024) void k_rms_norm_back(NormBackArgs a, int G) {
+// group is the workgroup, in LDS: the registers hold three tensors' vectors); the
+// groups of a workgroup add theirs in LDS (G VPT N floats) in order, and the
+// workgroup writes one row of partial sums.
+//
+// Loads and stores complete in one order, so loads that follow a row's stores
+// wait for them as well.  Where the registers hold two rows' vectors (AHEAD), the
+// next row's loads are issued a whole row ahead, and gamma, which would queue
+// behind them, stays in registers; other rows load dh between the two passes.  Rows
+// of one vector a lane run six waves a SIMD: two workgroups of ten waves put six on
+// some of them.  MI355X, BF16: 8192 x 5120 82 us (5.1 TB/s; without the load ahead
+// 92), 32768 x 2048 114 (139), 4096 x 8192 72 (79); FP32 1023 x 20479, one row a CU
+// and nothing ahead, 102 us (4.1 TB/s).
+template <typename T, int VPT, bool STREAM, bool WAVES>
+__global__ __launch_bounds__(1024, VPT * VecOf<T>::N <= 8 ? 6 : 4) void k_rms_norm_back(NormBackArgs a, int G) {
   constexpr int N = VecOf<T>::N;
   __shared__ float red[16];
   extern __shared__ float comb[];
   const int groups = blockDim.x / G;
-  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  // WAVES: a group is whole waves, so its row is the same all over a wave
+  const int at = threadIdx.x / G, grp = WAVES ? __builtin_amdgcn_readfirstlane(at) : at, j = threadIdx.x % G;
   constexpr bool IN_LDS = N == 4 && VPT >= 5;
-  float acc[IN_LDS ? 1 : VPT][N];
+  constexpr bool AHEAD = VPT * 8 <= 2 * N;
+  float acc[IN_LDS ? 1 : VPT][N], gamma[AHEAD ? VPT : 1][N];
 #pragma unroll
-  for (int k = 0; k < VPT; k++)
+  for (int k = 0; k < VPT; k++) {
+    const uint32_t c = (j + k * G) * N;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < N; i++) gamma[k][i] = 0.0f;
+      if (c < a.cols) load_gamma<N>(a.gamma, a.gamma_f32, c, (int)(a.cols - c), gamma[k]);
+    }
 #pragma unroll
     for (int i = 0; i < N; i++) {
       if constexpr (IN_LDS)
-        comb[(j + k * G) * N + i] = 0.0f;
+        comb[c + i] = 0.0f;
       else
         acc[k][i] = 0.0f;
     }
-  for (uint32_t r0 = blockIdx.x * groups; r0 < a.rows; r0 += gridDim.x * groups) {
+  }
+  auto load = [&](uint32_t r0, BackRow<VPT>& v) {
     const uint32_t row = r0 + grp;
     const bool live = row < a.rows;
-    const float rstd = live ? a.rstd[row] : 0.0f;
+    v.rstd = live ? a.rstd[row] : 0.0f;
     const T* dyr = static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy;
     const T* hr = static_cast<const T*>(a.h) + (int64_t)row * a.ld_h;
-    const T* dhr = static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh;
-    u32x4_t vy[VPT], vh[VPT], vd[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
       const int n = live ? (int)a.cols - (int)c : 0;
-      vy[k] = vh[k] = vd[k] = u32x4_t{0, 0, 0, 0};
+      v.dy[k] = v.h[k] = u32x4_t{0, 0, 0, 0};
       if (n > 0) {
-        vy[k] = load_vec<T, STREAM>(dyr + c, n);
-        vh[k] = load_vec<T, STREAM>(hr + c, n);
-        if (a.dh != nullptr) vd[k] = load_vec<T, STREAM>(dhr + c, n);
+        v.dy[k] = load_vec<T, STREAM>(dyr + c, n);
+        v.h[k] = load_vec<T, STREAM>(hr + c, n);
       }
+    }
+  };
+  auto load_dh = [&](uint32_t r0, BackRow<VPT>& v) {
+    const uint32_t row = r0 + grp;
+    const T* dhr = static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh;
+#pragma unroll
+    for (int k = 0; k < VPT; k++) {
+      const uint32_t c = (j + k * G) * N;
+      const int n = row < a.rows && a.dh != nullptr ? (int)a.cols - (int)c : 0;
+      v.dh[k] = u32x4_t{0, 0, 0, 0};
+      if (n > 0) v.dh[k] = load_vec<T, STREAM>(dhr + c, n);
+    }
+  };
+  const uint32_t step = gridDim.x * groups;
+  BackRow<VPT> next;
+  if constexpr (AHEAD) {
+    load(blockIdx.x * groups, next);
+    load_dh(blockIdx.x * groups, next);
+  }
+  for (uint32_t r0 = blockIdx.x * groups; r0 < a.rows; r0 += step) {
+    const uint32_t row = r0 + grp;
+    const int cols = row < a.rows ? (int)a.cols : 0;
+    BackRow<VPT> v;
+    if constexpr (AHEAD) {
+      v = next;
+      load(r0 + step, next);
+      load_dh(r0 + step, next);
+    } else {
+      load(r0, v);
     }
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
-      const int n = live ? (int)a.cols - (int)c : 0;
-      if (n <= 0) continue;
+      if ((int)c >= cols) continue;
       float dy[N], nh[N], g[N];
-      VecOf<T>::unpack(vy[k], dy);
-      VecOf<T>::unpack(vh[k], nh);
-      load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
-      float* sums = IN_LDS ? comb + (j + k * G) * N : acc[IN_LDS ? 0 : k];
+      VecOf<T>::unpack(v.dy[k], dy);
+      VecOf<T>::unpack(v.h[k], nh);
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int i = 0; i < N; i++) g[i] = gamma[k][i];
+      } else {
+        load_gamma<N>(a.gamma, a.gamma_f32, c, cols - (int)c, g);
+      }
+      float* sums = IN_LDS ? comb + c : acc[IN_LDS ? 0 : k];
 #pragma unroll
       for (int i = 0; i < N; i++) {
-        nh[i] *= rstd;
+        nh[i] *= v.rstd;
         s = __builtin_fmaf(dy[i] * g[i], nh[i], s);
         sums[i] = __builtin_fmaf(dy[i], nh[i], sums[i]);
       }
     }
+    if constexpr (!AHEAD) load_dh(r0, v);
     const float mean = group_sum(s, G, red) / (float)a.cols;
-    if (a.dx == nullptr && a.dr == nullptr) continue;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
-      const int n = live ? (int)a.cols - (int)c : 0;
-      if (n <= 0) continue;
-      float gy[N], nh[N], g[N];
-      VecOf<T>::unpack(vy[k], gy);
-      VecOf<T>::unpack(vh[k], nh);
-      load_gamma<N>(a.gamma, a.gamma_f32, c, n, g);
+      if ((int)c >= cols) continue;
+      float dy[N], h[N], gm[N], g[N];
+      VecOf<T>::unpack(v.dy[k], dy);
+      VecOf<T>::unpack(v.h[k], h);
+      VecOf<T>::unpack(v.dh[k], g);  // zeros without one
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        gy[i] *= g[i];
-        nh[i] *= rstd;
+        for (int i = 0; i < N; i++) gm[i] = gamma[k][i];
+      } else {
+        load_gamma<N>(a.gamma, a.gamma_f32, c, cols - (int)c, gm);
       }
-      back_vec<T, STREAM>(a, row, c, n, vd[k], gy, nh, rstd, mean);
+      back_vec<N>(g, dy, h, gm, v.rstd, mean);
+      back_store<T, STREAM>(a, row, c, cols - (int)c, g);
     }
   }
   if (a.partial == nullptr) return;
@@ -439,28 +521,26 @@ __global__ __launch_bounds__(1024) void k_rms_norm_back_wide(NormBackArgs a) {
     if (a.dx == nullptr && a.dr == nullptr) continue;
     for (int64_t c = (int64_t)threadIdx.x * N; c < a.cols; c += 1024 * N) {
       const int n = (int)min((int64_t)N, (int64_t)a.cols - c);
-      float gy[N], nh[N], g[N];
-      VecOf<T>::unpack(load_vec(dyr + c, n), gy);
-      VecOf<T>::unpack(load_vec(hr + c, n), nh);
-      load_gamma<N>(a.gamma, a.gamma_f32, (uint32_t)c, n, g);
-#pragma unroll
-      for (int i = 0; i < N; i++) {
-        gy[i] *= g[i];
-        nh[i] *= rstd;
-      }
-      const u32x4_t dh = a.dh == nullptr ? u32x4_t{0, 0, 0, 0}
-                                         : load_vec(static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh + c, n);
-      back_vec<T, true>(a, row, (uint32_t)c, n, dh, gy, nh, rstd, mean);
+      float dy[N], h[N], gm[N], g[N];
+      VecOf<T>::unpack(load_vec(dyr + c, n), dy);
+      VecOf<T>::unpack(load_vec(hr + c, n), h);
+      load_gamma<N>(a.gamma, a.gamma_f32, (uint32_t)c, n, gm);
+      VecOf<T>::unpack(a.dh == nullptr ? u32x4_t{0, 0, 0, 0}
+                                       : load_vec(static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh + c, n), g);
+      back_vec<N>(g, dy, h, gm, rstd, mean);
+      back_store<T, true>(a, row, (uint32_t)c, n, g);
     }
   }
 }
 
-// dgamma[c] = sum of the partial rows, in their order: eight slices of rows per
+// dgamma[c] = sum of the partial rows, in their order: 32 slices of rows per
 // column, added in LDS.
-__global__ __launch_bounds__(256) void k_dgamma(const float* partial, uint32_t parts, uint32_t cols, float* dgamma) {
-  __shared__ float part[8][32];
+constexpr int DG = 32;
+__global__ __launch_bounds__(DG * 32) void k_dgamma(const float* partial, uint32_t parts, uint32_t cols,
+                                                    float* dgamma) {
+  __shared__ float part[DG][32];
   const uint32_t lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const uint32_t p0 = parts * slice / 8, p1 = parts * (slice + 1) / 8;
+  const uint32_t p0 = parts * slice / DG, p1 = parts * (slice + 1) / DG;
   for (uint64_t base = blockIdx.x * 32; base < cols; base += (uint64_t)gridDim.x * 32) {
     const uint64_t c = base + lane;
     float s = 0.0f;
@@ -474,7 +554,7 @@ __global__ __launch_bounds__(256) void k_dgamma(const float* partial, uint32_t p
     if (slice == 0 && c < cols) {
       s = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; q++) s += part[q][lane];
+      for (int q = 0; q < DG; q++) s += part[q][lane];
       dgamma[c] = s;
     }
   }
@@ -583,7 +663,7 @@ BackShape back_shape(int64_t rows, int64_t cols, int N) {
   b.row = row_shape(vecs, vecs <= kBackThreads ? 1 : 2);
   if (b.row.vpt * N > 32) b.row = RowShape{0, 0};  // beyond the registers
   if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
-  b.groups = std::max(1, kBackThreads / b.row.G);
+  b.groups = std::max(1, 512 / b.row.G);
   const int64_t most = b.row.G * b.groups <= kBackThreads ? 2 * kCus : kCus;
   // few rows: two or more of them to each partial row
   if (rows <= 2 * kCus && b.row.G <= 512) b.groups = std::max(b.groups, 2);
@@ -608,7 +688,9 @@ hipError_t norm_back_t(const NormBackArgs& a, hipStream_t s) {
   hipError_t e = hipSuccess;
   with_vpt(r.vpt, [&](auto vpt) {
     constexpr int VPT = vpt.value * N <= 32 ? vpt.value : 1;  // what back_shape picks
-    auto* kernel = stream ? &k_rms_norm_back<T, VPT, true> : &k_rms_norm_back<T, VPT, false>;
+    auto* kernel = stream ? &k_rms_norm_back<T, VPT, true, true> : &k_rms_norm_back<T, VPT, false, true>;
+    if constexpr (VPT == 1)
+      if (r.G < 64) kernel = stream ? &k_rms_norm_back<T, 1, true, false> : &k_rms_norm_back<T, 1, false, false>;
     if (lds > 64 * 1024)
       e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e == hipSuccess) kernel<<<(unsigned)parts, groups * r.G, lds, s>>>(a, r.G);
@@ -655,7 +737,7 @@ hipError_t launch_rms_norm_back(const void* dy, const void* dh, const void* h, i
   }
   if (dgamma == nullptr) return hipSuccess;
   const unsigned grid = (unsigned)std::min<int64_t>((cols + 31) / 32, 1 << 20);  // lanes of a launch fit 32 bits
-  k_dgamma<<<grid, 256, 0, s>>>(partial, (uint32_t)parts, (uint32_t)cols, dgamma);
+  k_dgamma<<<grid, DG * 32, 0, s>>>(partial, (uint32_t)parts, (uint32_t)cols, dgamma);
   return hipGetLastError();
 }
 
