@@ -6,7 +6,7 @@
 // pair per token, and the label's logit; a second kernel joins a token's pairs.
 // Backward, on the tokens that have a label only, over pieces of the vocabulary:
 // the logits tile is formed again, d = dloss (exp(z - lse) - [v = label]) is held
-// as BF16 for the piece, and two products follow: dW = d^T x (whole per piece)
+// as BF16 for the piece (in what units, and when in two parts: Tokens, loss_device.hpp), and two products follow: dW = d^T x (whole per piece)
 // and dx += d W (FP32 in the workspace across pieces, rounded to BF16 once).
 //
 // Every product has its output's contiguous dimension as the tile's rows m, so a
@@ -124,14 +124,27 @@ __global__ __launch_bounds__(256) void k_loss(const float2* stats, int tiles, in
 
 // ---- backward: the tokens that have a label come first
 
+// The unit of d: 1 where the largest |dloss| m is no normal number (an infinity's quotients are NaN).
+__device__ __forceinline__ float scale_of(float m) { return m >= 0x1p-126f && m < INFINITY ? m : 1.0f; }
+
 // One workgroup: token t's place is the number of labelled tokens before it.
-__global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, int64_t T, int64_t V, Tokens tk) {
+__global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, const float* dloss, int64_t T, int64_t V,
+                                                 Tokens tk) {
   __shared__ int sums[1024];
+  __shared__ float tops[16];
   const int tid = threadIdx.x;
   const int64_t per = (T + 1023) / 1024, t0 = min(T, tid * per), t1 = min(T, t0 + per);
   int c = 0;
-  for (int64_t t = t0; t < t1; t++) c += labels[t] >= 0 && labels[t] < V ? 1 : 0;
+  float top = 0.0f;
+  for (int64_t t = t0; t < t1; t++)
+    if (labels[t] >= 0 && labels[t] < V) {
+      c++;
+      top = fmaxf(top, __builtin_fabsf(dloss[t]));
+    }
   sums[tid] = c;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
   __syncthreads();
   for (int o = 1; o < 1024; o <<= 1) {
     const int v = tid >= o ? sums[tid - o] : 0;
@@ -145,36 +158,50 @@ __global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, int64_t 
     tk.place[t] = valid ? at : -1;
     if (valid) tk.list[at++] = (int)t;
   }
-  if (tid == 1023) *tk.n = sums[1023];
+  if (tid != 1023) return;
+  *tk.n = sums[1023];
+  for (int q = 0; q < 16; q++) top = fmaxf(top, tops[q]);
+  *tk.scale = scale_of(top);
 }
 
 // Both of the above for up to FEW_LABELS tokens, one launch: every workgroup
 // counts the labels itself (those before its 8 tokens, and all of them).
 constexpr int64_t FEW_LABELS = 2048;
-__global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, int T, int64_t V, const uint16_t* x,
-                                                       int64_t ld_x, int64_t H, Tokens tk, uint16_t* xc) {
+__global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, const float* dloss, int T, int64_t V,
+                                                       const uint16_t* x, int64_t ld_x, int64_t H, Tokens tk,
+                                                       uint16_t* xc) {
   __shared__ int part[2][4];
+  __shared__ float tops[4];
   const int tid = threadIdx.x, first = blockIdx.x * 8;
   auto labelled = [&](int t) { return t < T && labels[t] >= 0 && labels[t] < V; };
   int before = 0, all = 0;
+  float top = 0.0f;
   for (int t = tid; t < T; t += 256) {
     const int v = labelled(t) ? 1 : 0;
     all += v;
     before += t < first ? v : 0;
+    if (v != 0 && blockIdx.x == 0) top = fmaxf(top, __builtin_fabsf(dloss[t]));
   }
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
     all += __shfl_xor(all, m, 64);
     before += __shfl_xor(before, m, 64);
+    top = fmaxf(top, __shfl_xor(top, m, 64));
   }
   if ((tid & 63) == 0) {
     part[0][tid >> 6] = before;
     part[1][tid >> 6] = all;
+    tops[tid >> 6] = top;
   }
   __syncthreads();
   int at = part[0][0] + part[0][1] + part[0][2] + part[0][3];
   const int n = part[1][0] + part[1][1] + part[1][2] + part[1][3];
-  if (blockIdx.x == 0 && tid == 0) *tk.n = n;
+  const bool two = n <= tk.half;
+  const int cols = n == 0 ? 0 : two ? tk.half + n : n;
+  if (blockIdx.x == 0 && tid == 0) {
+    *tk.n = n;
+    *tk.scale = scale_of(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+  }
   for (int t = first; t < first + 8; t++) {
     const bool valid = labelled(t);
     if (tid == 0 && t < T) {
@@ -182,27 +209,32 @@ __global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, in
       if (valid) tk.list[at] = t;
     }
     if (valid) {
-      for (int64_t c = tid * 8; c < H; c += 256 * 8)
-        *reinterpret_cast<u32x4_t*>(xc + at * H + c) = *reinterpret_cast<const u32x4_t*>(x + t * ld_x + c);
+      for (int64_t c = tid * 8; c < H; c += 256 * 8) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + t * ld_x + c);
+        *reinterpret_cast<u32x4_t*>(xc + at * H + c) = v;
+        if (two) *reinterpret_cast<u32x4_t*>(xc + (tk.half + at) * H + c) = v;
+      }
       at++;
     }
-    // the grid covers T up to a multiple of 128: its rows past n are zeros where K needs them
-    if (t >= n && t < (n + 127) / 128 * 128)
+    // the grid covers T up to a multiple of 128: rows without a token are zeros where K needs them
+    if (t >= n && t < (cols + 127) / 128 * 128 && !(two && t >= tk.half && t < cols))
       for (int64_t c = tid * 8; c < H; c += 256 * 8)
         *reinterpret_cast<u32x4_t*>(xc + t * H + c) = u32x4_t{0, 0, 0, 0};
   }
 }
 
 // xc[i] = x[list[i]] for the n labelled tokens (nothing else of x is read
-// again), then zeros up to a multiple of 128 rows (K of the dw product).
+// again), twice where d has two parts, and zeros elsewhere up to a multiple of 128
+// rows (K of the dw product).
 __global__ __launch_bounds__(256) void k_gather(const uint16_t* x, int64_t ld_x, int64_t H, Tokens tk, uint16_t* xc) {
   const int64_t i = blockIdx.x;
-  const int n = *tk.n;
-  if (i >= (n + 127) / 128 * 128) return;
-  const uint16_t* src = x + (i < n ? (int64_t)tk.list[i] * ld_x : 0);
+  const int n = *tk.n, cols = tk.columns();
+  if (i >= (cols + 127) / 128 * 128) return;
+  const int64_t at = tk.two() && i >= tk.half ? i - tk.half : i;
+  const uint16_t* src = x + (at < n ? (int64_t)tk.list[at] * ld_x : 0);
   for (int64_t c = threadIdx.x * 8; c < H; c += 256 * 8)
     *reinterpret_cast<u32x4_t*>(xc + i * H + c) =
-        i < n ? *reinterpret_cast<const u32x4_t*>(src + c) : u32x4_t{0, 0, 0, 0};
+        at < n ? *reinterpret_cast<const u32x4_t*>(src + c) : u32x4_t{0, 0, 0, 0};
 }
 
 // ---- a BF16 tile through LDS: rows n of 64 W values of m (8 W chunks of 16
@@ -219,9 +251,14 @@ __device__ __forceinline__ u32x4_t tile_get(const uint8_t* lds, int n, int g) {
   return *reinterpret_cast<const u32x4_t*>(lds + n * 128 * W + ((g ^ (n & (8 * W - 1))) << 4));
 }
 
+// What a value's BF16 leaves of it (nothing where that is infinite).
+__device__ __forceinline__ float rest(float v, float held) {
+  return __builtin_fabsf(held) == INFINITY ? 0.0f : v - held;
+}
+
 // d^T of a piece of the vocabulary, BF16 [rows up to a multiple of 128][ldd], one
-// column per labelled token, zeros in the columns from n up to a multiple of 128
-// and in the rows past the piece's last: both are K of a later product.
+// column per labelled token (or two, see Tokens), zeros in the other columns up to a
+// multiple of 128 and in the rows past the piece's last: both are K of a later product.
 template <int W, bool EVEN>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
                                                                  const uint16_t* xc, int H, int tiles_t, int64_t v_first,
@@ -250,7 +287,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
     if (i < n_tok) {
       const int t = tk.list[i];
       l = lse[t];
-      g = dloss[t];
+      g = dloss[t] / *tk.scale;
       lab = labels[t] - v_first - n0;
     }
     s_lse[threadIdx.x] = l;
@@ -264,12 +301,14 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
   const int lab0 = s_lab[wm * WAVE + lane] / WAVE, lab1 = s_lab[wm * WAVE + WAVE - 64 + lane] / WAVE;
   const bool hit = __any((s_lab[wm * WAVE + lane] >= 0 && lab0 == wn) ||
                          (s_lab[wm * WAVE + WAVE - 64 + lane] >= 0 && lab1 == wn));
-  auto put = [&](auto with_labels) {
+  const bool two = n_tok <= tk.half;
+  auto put = [&](auto with_labels, auto parts) {
 #pragma unroll
     for (int i = 0; i < W; i++)
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         const int m = wm * WAVE + 32 * i + 8 * q + 4 * h;
+        if (parts.value == 2 && m >= tk.half) continue;
         const float4 l = *reinterpret_cast<const float4*>(s_lse + m);
         const float4 g = *reinterpret_cast<const float4*>(s_g + m);
         int4 lab = make_int4(-1, -1, -1, -1);
@@ -285,15 +324,23 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
             p2 -= lab.z == n ? 1.0f : 0.0f;
             p3 -= lab.w == n ? 1.0f : 0.0f;
           }
-          tile_put<W>(lds, n, m >> 3, h, bf16_pack(p0 * g.x, p1 * g.y), bf16_pack(p2 * g.z, p3 * g.w));
+          p0 *= g.x, p1 *= g.y, p2 *= g.z, p3 *= g.w;
+          const uint32_t d01 = bf16_pack(p0, p1), d23 = bf16_pack(p2, p3);
+          tile_put<W>(lds, n, m >> 3, h, d01, d23);
+          if constexpr (parts.value == 2)
+            tile_put<W>(lds, n, (m + tk.half) >> 3, h, bf16_pack(rest(p0, bf16lo(d01)), rest(p1, bf16hi(d01))),
+                        bf16_pack(rest(p2, bf16lo(d23)), rest(p3, bf16hi(d23))));
         }
         __builtin_amdgcn_sched_barrier(0);  // few token values at a time beside 256 accumulators
       }
   };
-  if (hit)
-    put(std::true_type{});
+  using std::integral_constant;
+  if (two)
+    put(std::true_type{}, integral_constant<int, 2>{});
+  else if (hit)
+    put(std::true_type{}, integral_constant<int, 1>{});
   else
-    put(std::false_type{});
+    put(std::false_type{}, integral_constant<int, 1>{});
   __syncthreads();
   const int padded = (rows + 127) / 128 * 128;
   for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
@@ -301,12 +348,12 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
     const int c = m0 + 8 * g;
     if (n0 + n >= padded || c >= ldd) continue;
     u32x4_t v = {0, 0, 0, 0};
-    if (n0 + n < rows && c < n_tok) {
+    const int left = n_tok - (two && c >= tk.half ? c - tk.half : c);  // tokens from this column on
+    if (n0 + n < rows && left > 0) {
       v = tile_get<W>(lds, n, g);
-      if (c + 8 > n_tok) {
+      if (left < 8) {
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-          v[k] &= (c + 2 * k < n_tok ? 0xFFFFu : 0u) | (c + 2 * k + 1 < n_tok ? 0xFFFF0000u : 0u);
+        for (int k = 0; k < 4; k++) v[k] &= (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
       }
     }
     *reinterpret_cast<u32x4_t*>(d + (int64_t)(n0 + n) * ldd + c) = v;
@@ -319,18 +366,19 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint1
                                                         int rows, Tokens tk, OutT* dw, int64_t ld_dw, int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
-  const int n_tok = *tk.n;
+  const int cols = tk.columns();
+  const float scale = *tk.scale;
   int pm, pn;
   tile_place(blockIdx.x, (H + TILE - 1) / TILE, (rows + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
-  const int K = (n_tok + 127) / 128 * 128;
+  const int K = (cols + 127) / 128 * 128;
   floatx16 acc[W][W];
   constexpr bool SHORT = W == 2;  // few tokens: one LDS buffer, four workgroups per CU
   if (SHORT || K > 0) {
     const TileOperand ox{xc + m0, (uint32_t)H, H - m0, K};
     const TileOperand od{d + (int64_t)n0 * ldd, (uint32_t)ldd, rows - n0, K};
     if constexpr (SHORT)
-      tile_product_short<W, true, false>(ox, od, (n_tok + TILE_K - 1) / TILE_K, lds, acc);
+      tile_product_short<W, true, false>(ox, od, (cols + TILE_K - 1) / TILE_K, lds, acc);
     else
       tile_product<W, true, false, true>(ox, od, K, 0, K / TILE_K, lds, acc);
   } else {
@@ -355,7 +403,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint1
         OutT* out = dw + (int64_t)(n0 + n) * ld_dw + m0 + m;
         float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; r++) v[r] = acc[i][j][4 * q + r];
+        for (int r = 0; r < 4; r++) v[r] = acc[i][j][4 * q + r] * scale;
         if constexpr (sizeof(OutT) == 4) {
           if (!in) continue;
           float4* o = reinterpret_cast<float4*>(out);
@@ -386,7 +434,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint1
   }
 }
 
-// How the dx product of n labelled tokens is spread over `units` workgroups: its
+// How the dx product of n columns of d^T is spread over `units` workgroups: its
 // K (the vocabulary rows, `pairs` of 128 of them in a piece) is split into as many
 // parts as the units allow, each at least 256 rows deep.  Part p's sums are
 // rows p * rows .. of the workspace, FP32.
@@ -408,9 +456,10 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const u
                                                                          int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
-  const int n_tok = *tk.n;
+  const int n_tok = *tk.n, cols = tk.columns();
+  const bool two = tk.two();
   const int tiles_h = (H + TILE - 1) / TILE;
-  const DxSplit sp(n_tok, TILE, tiles_h, gridDim.x, (piece + 127) / 128);
+  const DxSplit sp(cols, TILE, tiles_h, gridDim.x, (piece + 127) / 128);
   if ((int)blockIdx.x >= tiles_h * sp.tiles * sp.parts) return;
   int pm, pn;
   tile_place(blockIdx.x, tiles_h, sp.tiles * sp.parts, pm, pn);
@@ -433,7 +482,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const u
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         const int m = m0 + wm * WAVE + 32 * i + 8 * q + 4 * h, n = n0 + wn * WAVE + 32 * j + lr;
-        if (n >= n_tok || m >= H) continue;
+        if (n >= cols || m >= H || (two && n >= n_tok && n < tk.half)) continue;
         float4* o = reinterpret_cast<float4*>(out + (int64_t)n * H + m);
         float4 s = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
         if (accumulate) {
@@ -445,24 +494,30 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const u
       }
 }
 
-// dx (BF16) from its FP32 sums, added in order; 0 for ignored tokens.  A
-// workgroup takes 1024 columns of a token.
+// dx (BF16) from its FP32 sums, added in order (the smaller part of d last); 0 for
+// ignored tokens.  A workgroup takes 1024 columns of a token.
 __global__ __launch_bounds__(256) void k_dx(const float* sum, int units, int side, int pairs, int H, Tokens tk,
                                             uint16_t* dx, int64_t ld) {
   const int64_t t = blockIdx.x;
   const int64_t i = tk.place[t];
-  const DxSplit sp(*tk.n, side, (H + side - 1) / side, units, pairs);
+  const DxSplit sp(tk.columns(), side, (H + side - 1) / side, units, pairs);
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
   if (c >= H) return;
   float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (i >= 0) {
-    const float4* p = reinterpret_cast<const float4*>(sum + i * H + c);
+    const float scale = *tk.scale;
     const int64_t step = sp.rows * H / 4;
+    auto add = [&](int64_t row) {
+      const float4* p = reinterpret_cast<const float4*>(sum + row * H + c);
 #pragma unroll 8
-    for (int q = 0; q < sp.parts; q++) {
-      const float4 v = p[q * step];
-      f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
-    }
+      for (int q = 0; q < sp.parts; q++) {
+        const float4 v = p[q * step];
+        f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
+      }
+    };
+    add(i);
+    if (tk.two()) add(tk.half + i);
+    f.x *= scale, f.y *= scale, f.z *= scale, f.w *= scale;
   }
   *reinterpret_cast<u32x2_t*>(dx + t * ld + c) = u32x2_t{bf16_pack(f.x, f.y), bf16_pack(f.z, f.w)};
 }
@@ -547,7 +602,7 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t H) {
   p.xc = up16(up128(p.piece) * p.ldd * 2);
   p.sum = p.xc + up16(up128(T) * H * 2);
   p.tok = p.sum + up16(p.dxp.units * tile_side(p.dxp.W) * tile_side(p.dxp.W) * 4);
-  p.end = p.tok + up16((2 * T + 1) * 4);
+  p.end = p.tok + up16((2 * T + 2) * 4);
   return p;
 }
 
@@ -632,12 +687,12 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
   uint16_t* xc = reinterpret_cast<uint16_t*>(ws + pl.xc);
   float* sum = reinterpret_cast<float*>(ws + pl.sum);
   int* tok = reinterpret_cast<int*>(ws + pl.tok);
-  const Tokens tk{tok, tok + 1, tok + 1 + T};
+  const Tokens tk{tok, reinterpret_cast<float*>(tok + 1), tok + 2, tok + 2 + T, T <= 16 ? 16 : T <= 32 ? 32 : 64};
   const uint16_t* xp = static_cast<const uint16_t*>(x);
   if (T <= FEW_LABELS) {
-    k_tokens_gather<<<(unsigned)(up128(T) / 8), 256, 0, s>>>(labels, (int)T, V, xp, ld_x, H, tk, xc);
+    k_tokens_gather<<<(unsigned)(up128(T) / 8), 256, 0, s>>>(labels, dloss, (int)T, V, xp, ld_x, H, tk, xc);
   } else {
-    k_tokens<<<1, 1024, 0, s>>>(labels, T, V, tk);
+    k_tokens<<<1, 1024, 0, s>>>(labels, dloss, T, V, tk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     k_gather<<<(unsigned)up128(T), 256, 0, s>>>(xp, ld_x, H, tk, xc);
   }

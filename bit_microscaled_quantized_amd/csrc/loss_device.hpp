@@ -33,10 +33,27 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 
 // What the backward pass knows of its n[0] labelled tokens, in order: which
 // tokens they are, and of every token its place among them (or -1).
+//
+// d is held in units of scale, the labelled tokens' largest |dloss|, which the
+// results are multiplied by in FP32.  Tokens of a mean loss share one dloss; in its
+// units a label that the model gives little is -1 and hardly rounded, where -dloss
+// itself would be rounded alike for all tokens, up to 2^-8 of the whole gradient.
+//
+// One BF16 rounding of d, 2^-8 of it at most, averages out over a gradient's many
+// terms, but a few tokens' gradients are one large term each (their labels'), and
+// then it doubles the error of the result's own rounding.  Up to `half` labelled
+// tokens d is therefore held in two parts, BF16 and the BF16 of what remains: token i
+// takes columns i and half + i of d^T, rows i and half + i of xc.  The products'
+// smallest tiles have the room, so this takes no longer.
 struct Tokens {
   int* n;
+  float* scale;
   int* place;
   int* list;
+  int half;
+  __device__ __forceinline__ bool two() const { return *n <= half; }
+  // columns of d^T up to the last in use (those between the parts are zeros)
+  __device__ __forceinline__ int columns() const { return *n == 0 ? 0 : two() ? half + *n : *n; }
 };
 
 // ---- the weight gradient of few tokens (loss_few.hip)
@@ -44,7 +61,7 @@ struct Tokens {
 constexpr int FEW_DW_TOKENS = 64;
 
 // dw (+)= dt^T xc for T <= FEW_DW_TOKENS; dt [rows][ldt] has zeros, and xc zero rows,
-// past the last token up to a multiple of 32
+// past the last column up to a multiple of 32
 hipError_t few_dw(const uint16_t* xc, int64_t H, const uint16_t* dt, int64_t ldt, int64_t rows, int64_t T, Tokens tk,
                   void* dw, int dw_f32, int64_t ld_dw, int accumulate, hipStream_t s);
 

@@ -36,14 +36,15 @@ __device__ __forceinline__ bf16x8_t block_column(const uint32_t (&rows)[8][C / 2
 
 // ---- dw[v][h] (+)= sum_t dt[v][t] xc[t][h]
 //
-// A wave holds 32 KT tokens of C columns per lane (128 columns in all) of xc in
+// A wave holds 32 KT rows (tokens, in two parts) of C columns per lane (128 columns in all) of xc in
 // registers and walks the vocabulary 16 rows at a time; the four waves take
 // adjacent columns of the same rows.
 template <int KT, typename OutT>
 __global__ __launch_bounds__(256) void k_few_dw(const uint16_t* xc, int H, const uint16_t* dt, int64_t ldt, int rows,
                                                 int slices, int parts, Tokens tk, OutT* dw, int64_t ld_dw,
                                                 int accumulate) {
-  const int kt = (*tk.n + 31) / 32;  // blocks of 32 tokens that hold any
+  const float scale = *tk.scale;
+  const int kt = (tk.columns() + 31) / 32;  // blocks of 32 columns that hold any
   const int slice = blockIdx.x % slices, part = blockIdx.x / slices;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int h = (slice * 4 + wave) * 16 * C + C * i;
@@ -97,7 +98,7 @@ __global__ __launch_bounds__(256) void k_few_dw(const uint16_t* xc, int H, const
       OutT* o = dw + (int64_t)v * ld_dw + h;
       float f[C];
 #pragma unroll
-      for (int j = 0; j < C; j++) f[j] = acc[j][r];
+      for (int j = 0; j < C; j++) f[j] = acc[j][r] * scale;
       if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
         for (int j = 0; j < C; j += 4) {
@@ -144,10 +145,12 @@ static hipError_t few_dw_t(const uint16_t* xc, int64_t H, const uint16_t* dt, in
         xc, (int)H, dt, ldt, (int)rows, (int)slices, (int)parts, tk, dw, ld_dw, accumulate);
   };
   using std::integral_constant;
-  if (T <= 32)
+  if (T <= 16)
     go(integral_constant<int, 1>{});
-  else
+  else if (T <= 32)
     go(integral_constant<int, 2>{});
+  else
+    go(integral_constant<int, 4>{});
   return hipGetLastError();
 }
 

@@ -119,7 +119,9 @@ nvfp4_status nvfp4_linear_cross_entropy(int64_t T, int64_t V, int64_t H, const v
  *   dx[t] = sum_v d[t][v] * w[v];   dw[v] = beta * dw[v] + sum_t d[t][v] * x[t]
  * Tokens whose label is outside [0, V) have d = 0, whatever their x, lse and
  * dloss hold.  The logits are formed again, in pieces of the vocabulary; each
- * d is held as BF16 (one rounding, within 2^-8) for the two products.
+ * d is held as BF16 for the two products, in units of the labelled tokens' largest
+ * |dloss| (one rounding, within 2^-8), and with up to 64 labelled tokens in two
+ * BF16 parts (within 2^-16).
  *   dx [T][ld_dx] BF16 (or NULL); dw [V][ld_dw] of type dw_dt (or NULL; not
  *   both); 16-byte aligned, ld times element size a multiple of 16.  beta is 0
  *   (overwrite) or 1 (accumulate; the sum is rounded once).  Other arguments as

@@ -155,6 +155,56 @@ def test_large_vocabularies_and_many_tokens(T, V, H):
     q.check_dw(dw, F32)
 
 
+@pytest.mark.parametrize("T,ignore", [(1, 0.0), (5, 0.3), (16, 0.0), (17, 0.0), (32, 0.1), (33, 0.0), (64, 0.0), (65, 0.1),
+                                      (300, 0.9), (2500, 0.98)])
+@pytest.mark.parametrize("V,H", [(1031, 264), (40, 128)])
+def test_few_labelled_tokens_keep_two_parts_of_d(T, ignore, V, H):
+    """Up to 64 labelled tokens the products see d within 2^-16 of it (BF16, and the BF16
+    of the rest: 2^-8 of 2^-8), so that FP32 dw and BF16 dx are that near."""
+    q = Head(T, V, H, ignore, seed=21).reference()
+    assert int(q.valid.sum()) <= 64
+    _, lse = q.forward()
+    dx, dw = q.backward(lse, F32)
+    q.dd = q.dd - q.d.abs() * (2.0 ** -8 - 2.0 ** -16)
+    q.check_dx(dx)
+    q.check_dw(dw, F32)
+
+
+@pytest.mark.parametrize("T", [100, 2500])
+def test_a_shared_dloss_is_not_rounded(T):
+    """Tokens of a mean loss whose labels the model gives little: d at the label is -dloss
+    (1 - p), p < 2^-9, and held as -dloss, so dw there is within 2^-9 of dloss per token
+    (and the sums' roundings), where BF16 of dloss = 1.0038 / 128 alone is off by 2^-8 of it."""
+    q = Head(T, 2003, 128, 0.0, seed=2, lean=False)
+    q.x.mul_(0.2)
+    q.dloss.fill_(1.00387 / 128)
+    q.reference()
+    _, lse = q.forward()
+    assert float((q.d.abs().amax(1) / q.dloss).min()) > 1 - 2.0 ** -9
+    _, dw = q.backward(lse, F32)
+    seen = q.torch.zeros(2003, dtype=q.torch.bool, device="cuda")
+    seen[q.labels] = True
+    ref = q.d.t() @ q.xd
+    rel = float((dw.double() - ref)[seen].norm() / ref[seen].norm())
+    assert rel < 2.0 ** -9, rel
+
+
+def test_dloss_of_no_normal_size():
+    """All zero: zero gradients.  Tiny or infinite: as products in FP32 give them."""
+    q = Head(70, 300, 64, 0.0, seed=4).reference()
+    torch = q.torch
+    _, lse = q.forward()
+    q.dloss.zero_()
+    dx, dw = q.backward(lse, F32)
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
+    q.dloss.fill_(1e-37)
+    _, dw = q.reference().backward(lse, F32)
+    assert float((dw.double() - q.d.t() @ q.xd).norm() / (q.d.t() @ q.xd).norm()) < 2.0 ** -7
+    q.dloss[3] = float("inf")
+    dx, dw = q.backward(lse, F32)
+    assert bool((~dx[3].isfinite()).all()) and bool(dx[4:].isfinite().all())
+
+
 def test_weight_rows_that_span_more_than_32_bits():
     """Vocabulary rows 2 MiB apart: from one piece's first row to its last is more than
     4 GiB, and some stages of the dx product end a few rows past that."""
