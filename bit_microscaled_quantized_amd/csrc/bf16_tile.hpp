@@ -1,5 +1,5 @@
 // One tile of a BF16 matrix product with FP32 accumulation on gfx950, 256 x 256
-// (W = 4) or 128 x 128 (W = 2):
+// (W = 4), 128 x 128 (W = 2) or 64 x 64 (W = 1, K along the rows only):
 //   acc(m, n) = sum_k A(m, k) B(n, k)
 // for operands that hold K along their rows (element (m, k) at p[m * ld + k]) or
 // down their columns (KMAJOR, element (m, k) at p[k * ld + m]).
@@ -17,7 +17,7 @@
 // the reads and fetches are placed between the matrix instructions by hand.
 // The small tile fits twice on a compute unit, so that one workgroup's start and
 // end overlap the other's products: it is for products with few large tiles or
-// few stages.
+// few stages; the smallest, four to a unit, for those that have few of these too.
 //
 // LDS layouts, both free of bank conflicts (64 banks of 4 bytes):
 //   * K along rows: rows of 128 bytes; the 16-byte chunk c of row r lies in
@@ -171,6 +171,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
   TileFetch<W, AMAJ> fa;
   TileFetch<W, BMAJ> fb;
   static_assert(EVEN || (!AMAJ && !BMAJ), "odd stages are for K along rows");
+  static_assert(W > 1 || (!AMAJ && !BMAJ), "64 columns are too few for the transposing layout");
   fa.init(a, wave, lane);
   fb.init(b, wave, lane);
   TileFrag<W, AMAJ> ra;
@@ -267,6 +268,10 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
       if (m < W) {                                                                                     \
         TILE_READ(rst, rs, 1 - (q), 2 * m);                                                            \
         TILE_READ(rst, rs, 1 - (q), 2 * m + 1);                                                        \
+        if (W == 1 && fetch) {                                                                         \
+          TILE_LOAD(kt, dst, x0);                                                                      \
+          TILE_LOAD(kt, dst, (x0) + 1);                                                                \
+        }                                                                                              \
       } else if (W == 4 && m < 12) {                                                                   \
         if (fetch) TILE_LOAD(kt, dst, (x0) + m - 4);                                                   \
       } else if (W == 2) {                                                                             \

@@ -33,7 +33,7 @@ __device__ __forceinline__ int tile_row(int i, int r) { return 32 * i + 8 * (r >
 // stats[t][vt] = the pair of token t and vocabulary tile vt; zlab[t] = the
 // logit of t's label.
 template <int W, bool EVEN>
-__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
                                                                   const uint16_t* x, uint32_t ld_x, int T, int H,
                                                                   const int64_t* labels, float2* stats, float* zlab) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -51,6 +51,8 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_stats(c
   float2 st[W];
 #pragma unroll
   for (int j = 0; j < W; j++) {
+    st[j] = make_float2(-INFINITY, 0.0f);
+    if (n0 + wn * WAVE + 32 * j >= T) continue;  // no tokens here
     const int t = n0 + wn * WAVE + 32 * j + lr;
     if (V - m0 < TILE) {
 #pragma unroll
@@ -164,18 +166,20 @@ __global__ __launch_bounds__(1024) void k_tokens(const int64_t* labels, const fl
   *tk.scale = scale_of(top);
 }
 
-// Both of the above for up to FEW_LABELS tokens, one launch: every workgroup
-// counts the labels itself (those before its 8 tokens, and all of them).
-constexpr int64_t FEW_LABELS = 2048;
+// k_tokens and k_gather for up to FEW_LABELS tokens, one launch: every workgroup
+// counts the labels itself (those before its 4 tokens, and all of them); a wave copies
+// a token.
+constexpr int64_t FEW_LABELS = 4096;
 __global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, const float* dloss, int T, int64_t V,
                                                        const uint16_t* x, int64_t ld_x, int64_t H, Tokens tk,
                                                        uint16_t* xc) {
   __shared__ int part[2][4];
   __shared__ float tops[4];
-  const int tid = threadIdx.x, first = blockIdx.x * 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, first = blockIdx.x * 4;
   auto labelled = [&](int t) { return t < T && labels[t] >= 0 && labels[t] < V; };
   int before = 0, all = 0;
   float top = 0.0f;
+  const uint64_t mine = __ballot(lane < 4 && labelled(first + lane));  // of the workgroup's tokens
   for (int t = tid; t < T; t += 256) {
     const int v = labelled(t) ? 1 : 0;
     all += v;
@@ -194,7 +198,6 @@ __global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, co
     tops[tid >> 6] = top;
   }
   __syncthreads();
-  int at = part[0][0] + part[0][1] + part[0][2] + part[0][3];
   const int n = part[1][0] + part[1][1] + part[1][2] + part[1][3];
   const bool two = n <= tk.half;
   const int cols = n == 0 ? 0 : two ? tk.half + n : n;
@@ -202,25 +205,24 @@ __global__ __launch_bounds__(256) void k_tokens_gather(const int64_t* labels, co
     *tk.n = n;
     *tk.scale = scale_of(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
   }
-  for (int t = first; t < first + 8; t++) {
-    const bool valid = labelled(t);
-    if (tid == 0 && t < T) {
-      tk.place[t] = valid ? at : -1;
-      if (valid) tk.list[at] = t;
-    }
-    if (valid) {
-      for (int64_t c = tid * 8; c < H; c += 256 * 8) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + t * ld_x + c);
-        *reinterpret_cast<u32x4_t*>(xc + at * H + c) = v;
-        if (two) *reinterpret_cast<u32x4_t*>(xc + (tk.half + at) * H + c) = v;
-      }
-      at++;
-    }
-    // the grid covers T up to a multiple of 128: rows without a token are zeros where K needs them
-    if (t >= n && t < (cols + 127) / 128 * 128 && !(two && t >= tk.half && t < cols))
-      for (int64_t c = tid * 8; c < H; c += 256 * 8)
-        *reinterpret_cast<u32x4_t*>(xc + t * H + c) = u32x4_t{0, 0, 0, 0};
+  const int t = first + wave;
+  const bool valid = (mine >> wave) & 1;
+  const int at = part[0][0] + part[0][1] + part[0][2] + part[0][3] + __popcll(mine & ((1u << wave) - 1));
+  if (lane == 0 && t < T) {
+    tk.place[t] = valid ? at : -1;
+    if (valid) tk.list[at] = t;
   }
+  if (valid) {
+#pragma unroll 4
+    for (int64_t c = lane * 8; c < H; c += 64 * 8) {
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + t * ld_x + c);
+      *reinterpret_cast<u32x4_t*>(xc + at * H + c) = v;
+      if (two) *reinterpret_cast<u32x4_t*>(xc + (tk.half + at) * H + c) = v;
+    }
+  }
+  // the grid covers T up to a multiple of 128: rows without a token are zeros where K needs them
+  if (t >= n && t < (cols + 127) / 128 * 128 && !(two && t >= tk.half && t < cols))
+    for (int64_t c = lane * 8; c < H; c += 64 * 8) *reinterpret_cast<u32x4_t*>(xc + t * H + c) = u32x4_t{0, 0, 0, 0};
 }
 
 // xc[i] = x[list[i]] for the n labelled tokens (nothing else of x is read
@@ -260,17 +262,41 @@ __device__ __forceinline__ float rest(float v, float held) {
 // column per labelled token (or two, see Tokens), zeros in the other columns up to a
 // multiple of 128 and in the rows past the piece's last: both are K of a later product.
 template <int W, bool EVEN>
-__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
                                                                  const uint16_t* xc, int H, int tiles_t, int64_t v_first,
                                                                  Tokens tk, const int64_t* labels, const float* lse,
                                                                  const float* dloss, uint16_t* d, int64_t ldd) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int n_tok = *tk.n;
+  const int padded = (rows + 127) / 128 * 128;
   int pm, pn;  // token tile, vocabulary tile
-  tile_place(blockIdx.x, tiles_t, (rows + TILE - 1) / TILE, pm, pn);
+  tile_place(blockIdx.x, tiles_t, (padded + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
-  if (m0 >= n_tok) return;
+  const bool two = n_tok <= tk.half;  // then the first tile of tokens holds all, and writes both parts
+  if (m0 >= (two ? min(n_tok, 1) : (n_tok + 127) / 128 * 128)) return;
+  // Columns first .. end - 1 of d^T from the tile in LDS, which starts with token m0.
+  auto store = [&](int first, int end) {
+    for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
+      const int n = e / (8 * W), g = e % (8 * W);
+      const int c = first + 8 * g, left = n_tok - m0 - 8 * g;  // tokens from this column on
+      if (n0 + n >= padded || c >= end) continue;
+      u32x4_t v = {0, 0, 0, 0};
+      if (n0 + n < rows && left > 0) {
+        v = tile_get<W>(lds, n, g);
+        if (left < 8) {
+#pragma unroll
+          for (int k = 0; k < 4; k++) v[k] &= (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
+        }
+      }
+      *reinterpret_cast<u32x4_t*>(d + (int64_t)(n0 + n) * ldd + c) = v;
+    }
+  };
+  if (W == 1 && (m0 >= n_tok || n0 >= rows)) {  // only zeros
+    store(m0, two ? tk.half : (int)ldd);
+    if (two) store(tk.half, (int)ldd);
+    return;
+  }
   floatx16 acc[W][W];
   tile_product<W, false, false, EVEN>(TileOperand{xc + (int64_t)m0 * H, (uint32_t)H, n_tok - m0, H},
                              TileOperand{w + (int64_t)n0 * ld_w, ld_w, rows - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
@@ -298,17 +324,16 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, lr = lane & 31;
   // a label of the wave's tokens among its vocabulary rows?  (-1 stays -1)
-  const int lab0 = s_lab[wm * WAVE + lane] / WAVE, lab1 = s_lab[wm * WAVE + WAVE - 64 + lane] / WAVE;
-  const bool hit = __any((s_lab[wm * WAVE + lane] >= 0 && lab0 == wn) ||
-                         (s_lab[wm * WAVE + WAVE - 64 + lane] >= 0 && lab1 == wn));
-  const bool two = n_tok <= tk.half;
-  auto put = [&](auto with_labels, auto parts) {
+  const int lab0 = s_lab[wm * WAVE + (lane & (WAVE - 1))], lab1 = s_lab[wm * WAVE + WAVE - 1 - (lane & (WAVE - 1))];
+  const bool hit = __any((lab0 >= 0 && lab0 / WAVE == wn) || (lab1 >= 0 && lab1 / WAVE == wn));
+  // PART 1: what BF16 leaves of d
+  auto put = [&](auto with_labels, auto part) {
 #pragma unroll
-    for (int i = 0; i < W; i++)
+    for (int i = 0; i < W; i++) {
+      if (m0 + wm * WAVE + 32 * i >= n_tok) continue;  // no tokens here
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         const int m = wm * WAVE + 32 * i + 8 * q + 4 * h;
-        if (parts.value == 2 && m >= tk.half) continue;
         const float4 l = *reinterpret_cast<const float4*>(s_lse + m);
         const float4 g = *reinterpret_cast<const float4*>(s_g + m);
         int4 lab = make_int4(-1, -1, -1, -1);
@@ -325,44 +350,39 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_logits_grad(co
             p3 -= lab.w == n ? 1.0f : 0.0f;
           }
           p0 *= g.x, p1 *= g.y, p2 *= g.z, p3 *= g.w;
-          const uint32_t d01 = bf16_pack(p0, p1), d23 = bf16_pack(p2, p3);
+          uint32_t d01 = bf16_pack(p0, p1), d23 = bf16_pack(p2, p3);
+          if constexpr (part.value == 1) {
+            d01 = bf16_pack(rest(p0, bf16lo(d01)), rest(p1, bf16hi(d01)));
+            d23 = bf16_pack(rest(p2, bf16lo(d23)), rest(p3, bf16hi(d23)));
+          }
           tile_put<W>(lds, n, m >> 3, h, d01, d23);
-          if constexpr (parts.value == 2)
-            tile_put<W>(lds, n, (m + tk.half) >> 3, h, bf16_pack(rest(p0, bf16lo(d01)), rest(p1, bf16hi(d01))),
-                        bf16_pack(rest(p2, bf16lo(d23)), rest(p3, bf16hi(d23))));
         }
         __builtin_amdgcn_sched_barrier(0);  // few token values at a time beside 256 accumulators
       }
+    }
   };
   using std::integral_constant;
-  if (two)
-    put(std::true_type{}, integral_constant<int, 2>{});
-  else if (hit)
+  if (two) {
+    put(std::true_type{}, integral_constant<int, 0>{});
+    __syncthreads();
+    store(m0, tk.half);
+    __syncthreads();
     put(std::true_type{}, integral_constant<int, 1>{});
-  else
-    put(std::false_type{}, integral_constant<int, 1>{});
-  __syncthreads();
-  const int padded = (rows + 127) / 128 * 128;
-  for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
-    const int n = e / (8 * W), g = e % (8 * W);
-    const int c = m0 + 8 * g;
-    if (n0 + n >= padded || c >= ldd) continue;
-    u32x4_t v = {0, 0, 0, 0};
-    const int left = n_tok - (two && c >= tk.half ? c - tk.half : c);  // tokens from this column on
-    if (n0 + n < rows && left > 0) {
-      v = tile_get<W>(lds, n, g);
-      if (left < 8) {
-#pragma unroll
-        for (int k = 0; k < 4; k++) v[k] &= (2 * k < left ? 0xFFFFu : 0u) | (2 * k + 1 < left ? 0xFFFF0000u : 0u);
-      }
-    }
-    *reinterpret_cast<u32x4_t*>(d + (int64_t)(n0 + n) * ldd + c) = v;
+    __syncthreads();
+    store(tk.half, (int)ldd);
+    return;
   }
+  if (hit)
+    put(std::true_type{}, integral_constant<int, 0>{});
+  else
+    put(std::false_type{}, integral_constant<int, 0>{});
+  __syncthreads();
+  store(m0, (int)ldd);
 }
 
 // dw[v][h] (+)= sum over the labelled tokens of d^T[v][i] xc[i][h]
-template <int W, typename OutT>
-__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint16_t* xc, int H, const uint16_t* d, int64_t ldd,
+template <int W, bool SHORT, typename OutT>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : SHORT ? 4 : 2) void k_dw(const uint16_t* xc, int H, const uint16_t* d, int64_t ldd,
                                                         int rows, Tokens tk, OutT* dw, int64_t ld_dw, int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
@@ -373,7 +393,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 4) void k_dw(const uint1
   const int m0 = pm * TILE, n0 = pn * TILE;
   const int K = (cols + 127) / 128 * 128;
   floatx16 acc[W][W];
-  constexpr bool SHORT = W == 2;  // few tokens: one LDS buffer, four workgroups per CU
+  // SHORT: one LDS buffer, four workgroups per CU
   if (SHORT || K > 0) {
     const TileOperand ox{xc + m0, (uint32_t)H, H - m0, K};
     const TileOperand od{d + (int64_t)n0 * ldd, (uint32_t)ldd, rows - n0, K};
@@ -495,28 +515,46 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const u
 }
 
 // dx (BF16) from its FP32 sums, added in order (the smaller part of d last); 0 for
-// ignored tokens.  A workgroup takes 1024 columns of a token.
+// ignored tokens.  A workgroup takes 1024 / S columns of a token, S slices of its
+// parts at a time: S = 8 for many parts (5 tokens, H = 152, 256 parts: 7 us against
+// 26), 1 for few (248 tokens, H = 4416: 6 us against 15).
+template <int S>
 __global__ __launch_bounds__(256) void k_dx(const float* sum, int units, int side, int pairs, int H, Tokens tk,
                                             uint16_t* dx, int64_t ld) {
+  __shared__ float4 slices[S == 1 ? 1 : S][S == 1 ? 1 : 256 / S];
   const int64_t t = blockIdx.x;
   const int64_t i = tk.place[t];
   const DxSplit sp(tk.columns(), side, (H + side - 1) / side, units, pairs);
-  const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
-  if (c >= H) return;
+  const int lane = threadIdx.x % (256 / S), slice = threadIdx.x / (256 / S);
+  const int c = (blockIdx.y * (256 / S) + lane) * 4;
   float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (i >= 0) {
-    const float scale = *tk.scale;
+  if (i >= 0 && c < H) {
     const int64_t step = sp.rows * H / 4;
+    const int p0 = sp.parts * slice / S, p1 = sp.parts * (slice + 1) / S;
     auto add = [&](int64_t row) {
       const float4* p = reinterpret_cast<const float4*>(sum + row * H + c);
 #pragma unroll 8
-      for (int q = 0; q < sp.parts; q++) {
+      for (int q = p0; q < p1; q++) {
         const float4 v = p[q * step];
         f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
       }
     };
     add(i);
     if (tk.two()) add(tk.half + i);
+  }
+  if constexpr (S > 1) {
+    slices[slice][lane] = f;
+    __syncthreads();
+    if (slice > 0) return;
+#pragma unroll
+    for (int q = 1; q < S; q++) {
+      const float4 v = slices[q][lane];
+      f.x += v.x, f.y += v.y, f.z += v.z, f.w += v.w;
+    }
+  }
+  if (c >= H) return;
+  if (i >= 0) {
+    const float scale = *tk.scale;
     f.x *= scale, f.y *= scale, f.z *= scale, f.w *= scale;
   }
   *reinterpret_cast<u32x2_t*>(dx + t * ld + c) = u32x2_t{bf16_pack(f.x, f.y), bf16_pack(f.z, f.w)};
@@ -543,9 +581,15 @@ int64_t piece_rows(int64_t T, int64_t V) {
 // workgroups over a 256-CU MI355X (one large tile per CU, two small ones) take
 // less.  Measured (H = 5120 and 2048, V = 10000 .. 131072, T = 64 .. 1000): a round
 // of large tiles takes 1.55 us a stage and 10 us around them, one of small tiles
-// 1.05 and 4, or 0.75 a stage where each has its CU to itself.
+// 1.05 and 4, or 0.75 a stage where each has its CU to itself; of 64 x 64 tiles four
+// take 0.7 and 4, two 0.5 and 3.
 double round_us(int64_t tiles, double stages, int W) {
   if (W == 4) return (double)((tiles + 255) / 256) * (stages * 1.55 + 10.0);
+  if (W == 1) {
+    const int64_t rest = tiles % 1024;
+    return (double)(tiles / 1024) * (stages * 0.7 + 4.0) +
+           (rest == 0 ? 0.0 : rest <= 512 ? stages * 0.5 + 3.0 : stages * 0.7 + 4.0);
+  }
   const int64_t rest = tiles % 512;
   return (double)(tiles / 512) * (stages * 1.05 + 4.0) +
          (rest == 0 ? 0.0 : stages * (rest <= 256 ? 0.75 : 1.05) + 4.0);
@@ -555,9 +599,19 @@ int tile_w(int64_t M, int64_t N, int64_t K) {
   const double large = round_us(tiles_of(M, 4) * tiles_of(N, 4), stages, 4);
   return large <= round_us(tiles_of(M, 2) * tiles_of(N, 2), stages, 2) ? 4 : 2;
 }
+// The same with 64 x 64 tiles, four to a CU: they leave fewer CUs idle and waste less
+// on a few tokens, but read LDS twice as often per product (MI355X, forward: 69 x 14757
+// x 3160 32 us against 46 with 128 x 128, 496 x 4707 x 4416 40 against 53; 257 x
+// 49999 x 2048 97 against 85).
+int logits_w(int64_t M, int64_t N, int64_t K) {
+  const double stages = (double)((K + TILE_K - 1) / TILE_K);
+  const int w = tile_w(M, N, K);
+  return round_us(tiles_of(M, 1) * tiles_of(N, 1), stages, 1) < round_us(tiles_of(M, w) * tiles_of(N, w), stages, w) ? 1
+                                                                                                                     : w;
+}
 
 // Up to here the dw product has few enough stages that four small tiles per CU,
-// each unpipelined, beat one large tile (131072 x 5120: 0.63 against 0.76 ms at 256
+// each unpipelined, beat one large tile, where there are that many (131072 x 5120: 0.63 against 0.76 ms at 256
 // tokens, 1.49 against 1.59 at 1000, 2.75 against 2.61 at 2000).
 constexpr int64_t SHORT_DW_TOKENS = 1536;
 
@@ -596,7 +650,7 @@ struct BackPlan {
 BackPlan back_plan(int64_t T, int64_t V, int64_t H) {
   BackPlan p;
   p.piece = piece_rows(T, V);
-  p.ldd = up128(T);
+  p.ldd = T <= 16 ? 32 : T <= 32 ? 64 : up128(T);  // up to 64 tokens have two columns each
   p.dxp = dx_plan(T, H, p.piece);
   p.d = 0;
   p.xc = up16(up128(p.piece) * p.ldd * 2);
@@ -623,8 +677,10 @@ hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
     allow(reinterpret_cast<const void*>(&k_logits_grad<4, false>), 4);
     allow(reinterpret_cast<const void*>(&k_logits_grad<2, true>), 2);
     allow(reinterpret_cast<const void*>(&k_logits_grad<2, false>), 2);
-    allow(reinterpret_cast<const void*>(&k_dw<4, uint16_t>), 4);
-    allow(reinterpret_cast<const void*>(&k_dw<4, float>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, uint16_t>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, float>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<2, false, uint16_t>), 2);
+    allow(reinterpret_cast<const void*>(&k_dw<2, false, float>), 2);
     allow(reinterpret_cast<const void*>(&k_dx_sum<4>), 4);
     allow(reinterpret_cast<const void*>(&k_dx_sum<2>), 2);
   });
@@ -642,11 +698,19 @@ hipError_t with_tile(int W, bool even, F&& f) {
     even ? f(integral_constant<int, 2>{}, std::true_type{}) : f(integral_constant<int, 2>{}, std::false_type{});
   return hipGetLastError();
 }
+// The same with 64 x 64 tiles too.
+template <typename F>
+hipError_t with_logits_tile(int W, bool even, F&& f) {
+  if (W > 1) return with_tile(W, even, f);
+  using std::integral_constant;
+  even ? f(integral_constant<int, 1>{}, std::true_type{}) : f(integral_constant<int, 1>{}, std::false_type{});
+  return hipGetLastError();
+}
 
 }  // namespace
 
 int64_t linear_ce_workspace(int64_t T, int64_t V, int64_t H, bool train) {
-  const int64_t fwd = up16(tiles_of(V, tile_w(V, T, H)) * T * 8) + up16(T * 4);
+  const int64_t fwd = up16(tiles_of(V, logits_w(V, T, H)) * T * 8) + up16(T * 4);
   return train ? std::max(fwd, back_plan(T, V, H).end) : fwd;
 }
 
@@ -655,11 +719,11 @@ hipError_t launch_linear_ce(int64_t T, int64_t V, int64_t H, const void* x, int6
   if (T == 0) return hipSuccess;
   hipError_t e = allow_lds();
   if (e != hipSuccess) return e;
-  const int w_tile = tile_w(V, T, H);
+  const int w_tile = logits_w(V, T, H);
   const int64_t tiles = tiles_of(V, w_tile);
   float2* stats = static_cast<float2*>(workspace);
   float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16(tiles * T * 8));
-  e = with_tile(w_tile, H % 128 == 0, [&](auto W, auto even) {
+  e = with_logits_tile(w_tile, H % 128 == 0, [&](auto W, auto even) {
     k_logits_stats<W.value, even.value><<<(unsigned)(tiles * tiles_of(T, W.value)), TILE_THREADS, lds_of(W.value), s>>>(
         static_cast<const uint16_t*>(w), (uint32_t)ld_w, (int)V, static_cast<const uint16_t*>(x), (uint32_t)ld_x, (int)T,
         (int)H, labels, stats, zlab);
@@ -690,7 +754,7 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
   const Tokens tk{tok, reinterpret_cast<float*>(tok + 1), tok + 2, tok + 2 + T, T <= 16 ? 16 : T <= 32 ? 32 : 64};
   const uint16_t* xp = static_cast<const uint16_t*>(x);
   if (T <= FEW_LABELS) {
-    k_tokens_gather<<<(unsigned)(up128(T) / 8), 256, 0, s>>>(labels, dloss, (int)T, V, xp, ld_x, H, tk, xc);
+    k_tokens_gather<<<(unsigned)(up128(T) / 4), 256, 0, s>>>(labels, dloss, (int)T, V, xp, ld_x, H, tk, xc);
   } else {
     k_tokens<<<1, 1024, 0, s>>>(labels, dloss, T, V, tk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -700,8 +764,9 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
     const int64_t n = std::min(pl.piece, V - v0);
     const uint16_t* wp = static_cast<const uint16_t*>(w) + v0 * ld_w;
-    e = with_tile(tile_w(T, n, H), H % 128 == 0, [&](auto W, auto even) {
-      const int64_t tt = tiles_of(T, W.value), tv = tiles_of(n, W.value);
+    e = with_logits_tile(logits_w(T, n, H), H % 128 == 0, [&](auto W, auto even) {
+      // up to 64 tokens are all in the first tile, in two parts
+      const int64_t tt = T <= 64 ? 1 : tiles_of(up128(T), W.value), tv = tiles_of(up128(n), W.value);
       k_logits_grad<W.value, even.value><<<(unsigned)(tt * tv), TILE_THREADS, lds_of(W.value), s>>>(
           wp, (uint32_t)ld_w, (int)n, xc, (int)H, (int)tt, v0, tk, labels, lse, dloss, d, pl.ldd);
     });
@@ -711,16 +776,25 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
       if (T <= FEW_DW_TOKENS) {
         e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, s);
       } else {
-        e = with_tile(T <= SHORT_DW_TOKENS ? 2 : 4, true, [&](auto W, auto) {
+        auto go = [&](auto W, auto with_short) {
+          constexpr bool SHORT = with_short.value;
           const unsigned grid = (unsigned)(tiles_of(H, W.value) * tiles_of(n, W.value));
-          const int lds = W.value == 2 ? tile_lds(2) / 2 : lds_of(W.value);
+          const int lds = SHORT ? tile_lds(W.value) / 2 : lds_of(W.value);
           if (dw_dt == 0)
-            k_dw<W.value><<<grid, TILE_THREADS, lds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk,
-                                                                 reinterpret_cast<uint16_t*>(out), ld_dw, accumulate);
+            k_dw<W.value, SHORT><<<grid, TILE_THREADS, lds, s>>>(
+                xc, (int)H, d, pl.ldd, (int)n, tk, reinterpret_cast<uint16_t*>(out), ld_dw, accumulate);
           else
-            k_dw<W.value><<<grid, TILE_THREADS, lds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk,
-                                                                 reinterpret_cast<float*>(out), ld_dw, accumulate);
-        });
+            k_dw<W.value, SHORT><<<grid, TILE_THREADS, lds, s>>>(
+                xc, (int)H, d, pl.ldd, (int)n, tk, reinterpret_cast<float*>(out), ld_dw, accumulate);
+          return hipGetLastError();
+        };
+        using std::integral_constant;
+        if (T <= SHORT_DW_TOKENS && tiles_of(H, 2) * tiles_of(n, 2) > 512)
+          e = go(integral_constant<int, 2>{}, std::true_type{});
+        else if (tile_w(H, n, T) == 2)
+          e = go(integral_constant<int, 2>{}, std::false_type{});
+        else
+          e = go(integral_constant<int, 4>{}, std::false_type{});
       }
       if (e != hipSuccess) return e;
     }
@@ -733,9 +807,15 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     }
   }
   if (dx == nullptr) return hipSuccess;
-  k_dx<<<dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), 256, 0, s>>>(
-      sum, (int)pl.dxp.units, tile_side(pl.dxp.W), (int)((pl.piece + 127) / 128), (int)H, tk, static_cast<uint16_t*>(dx),
-      ld_dx);
+  auto join = [&](auto S) {
+    k_dx<S.value><<<dim3((unsigned)T, (unsigned)((H * S.value + 1023) / 1024)), 256, 0, s>>>(
+        sum, (int)pl.dxp.units, tile_side(pl.dxp.W), (int)((pl.piece + 127) / 128), (int)H, tk,
+        static_cast<uint16_t*>(dx), ld_dx);
+  };
+  if (pl.dxp.units >= 16 * tiles_of(T, pl.dxp.W) * tiles_of(H, pl.dxp.W))  // 16 parts or more
+    join(std::integral_constant<int, 8>{});
+  else
+    join(std::integral_constant<int, 1>{});
   return hipGetLastError();
 }
 
