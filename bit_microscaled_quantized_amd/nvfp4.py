@@ -115,11 +115,23 @@ def _addr(t):
     return t.data_ptr()
 
 
+_current = None
+
+
+def _current_stream():
+    """Handle of torch's current stream.  The handle itself: building a Stream object takes
+    2.5 us more, half of a small call."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_device()  # initializes the device
+        _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
+    return _current[0](_current[1]())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        # the handle itself: building a Stream object takes 2.5 us more, half of a small call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
