@@ -10,6 +10,10 @@
 
 namespace nvfp4 {
 
+// Bytes from which on a launch streams past the caches (256 MB hold little of it
+// until the next reader comes).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+
 hipError_t launch_dropout(const void* x, int dt, int64_t rows, int64_t cols, int64_t ld_x, float p, uint64_t seed,
                           void* y, int64_t ld_y, hipStream_t s);
 

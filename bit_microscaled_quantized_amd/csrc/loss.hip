@@ -32,7 +32,7 @@ __device__ __forceinline__ int tile_row(int i, int r) { return 32 * i + 8 * (r >
 
 // stats[t][vt] = the pair of token t and vocabulary tile vt; zlab[t] = the
 // logit of t's label.
-template <int W, bool EVEN>
+template <int W, bool EVEN, bool ONCE>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_logits_stats(const uint16_t* w, uint32_t ld_w, int V,
                                                                   const uint16_t* x, uint32_t ld_x, int T, int H,
                                                                   const int64_t* labels, float2* stats, float* zlab) {
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_l
   tile_place(blockIdx.x, (V + TILE - 1) / TILE, (T + TILE - 1) / TILE, pm, pn);
   const int m0 = pm * TILE, n0 = pn * TILE;
   floatx16 acc[W][W];
-  tile_product<W, false, false, EVEN>(TileOperand{w + (int64_t)m0 * ld_w, ld_w, V - m0, H},
+  tile_product<W, false, false, EVEN>(TileOperand{w + (int64_t)m0 * ld_w, ld_w, V - m0, H, ONCE},
                              TileOperand{x + (int64_t)n0 * ld_x, ld_x, T - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -261,7 +261,7 @@ __device__ __forceinline__ float rest(float v, float held) {
 // d^T of a piece of the vocabulary, BF16 [rows up to a multiple of 128][ldd], one
 // column per labelled token (or two, see Tokens), zeros in the other columns up to a
 // multiple of 128 and in the rows past the piece's last: both are K of a later product.
-template <int W, bool EVEN>
+template <int W, bool EVEN, bool ONCE>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_logits_grad(const uint16_t* w, uint32_t ld_w, int rows,
                                                                  const uint16_t* xc, int H, int tiles_t, int64_t v_first,
                                                                  Tokens tk, const int64_t* labels, const float* lse,
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_l
   }
   floatx16 acc[W][W];
   tile_product<W, false, false, EVEN>(TileOperand{xc + (int64_t)m0 * H, (uint32_t)H, n_tok - m0, H},
-                             TileOperand{w + (int64_t)n0 * ld_w, ld_w, rows - n0, H}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
+                             TileOperand{w + (int64_t)n0 * ld_w, ld_w, rows - n0, H, ONCE}, H, 0, (H + TILE_K - 1) / TILE_K, lds,
                              acc);
   // what the tile's tokens hold: lse, dloss, and the label's row in this tile (or -1)
   __syncthreads();
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_l
 }
 
 // dw[v][h] (+)= sum over the labelled tokens of d^T[v][i] xc[i][h]
-template <int W, bool SHORT, typename OutT>
+template <int W, bool SHORT, bool STREAM, typename OutT>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : SHORT ? 4 : 2) void k_dw(const uint16_t* xc, int H, const uint16_t* d, int64_t ldd,
                                                         int rows, Tokens tk, OutT* dw, int64_t ld_dw, int accumulate) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -389,7 +389,10 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : SHORT ? 4 : 2) void k_dw
   const int cols = tk.columns();
   const float scale = *tk.scale;
   int pm, pn;
-  tile_place(blockIdx.x, (H + TILE - 1) / TILE, (rows + TILE - 1) / TILE, pm, pn);
+  // SHORT: few tokens' xc stays in L2 whole, so dw's rows are written from end to end
+  // (131072 x 5120, 128 tokens: the whole call 724 us against 785 in groups of 8)
+  const int tiles_h = (H + TILE - 1) / TILE;
+  tile_place(blockIdx.x, tiles_h, (rows + TILE - 1) / TILE, pm, pn, SHORT ? tiles_h : 8);
   const int m0 = pm * TILE, n0 = pn * TILE;
   const int K = (cols + 127) / 128 * 128;
   floatx16 acc[W][W];
@@ -432,7 +435,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : SHORT ? 4 : 2) void k_dw
             const float4 old = *o;
             s = make_float4(old.x + s.x, old.y + s.y, old.z + s.z, old.w + s.w);
           }
-          *o = s;
+          store16<STREAM>(o, __builtin_bit_cast(u32x4_t, s));
         } else {
           if (accumulate && in) {
             const u32x2_t old = *reinterpret_cast<const u32x2_t*>(out);
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : SHORT ? 4 : 2) void k_dw
     for (int e = threadIdx.x; e < TILE * 8 * W; e += TILE_THREADS) {
       const int n = e / (8 * W), g = e % (8 * W);
       if (n0 + n < rows && m0 + 8 * g < H)
-        *reinterpret_cast<u32x4_t*>(dw + (int64_t)(n0 + n) * ld_dw + m0 + 8 * g) = tile_get<W>(lds, n, g);
+        store16<STREAM>(dw + (int64_t)(n0 + n) * ld_dw + m0 + 8 * g, tile_get<W>(lds, n, g));
     }
   }
 }
@@ -469,7 +472,7 @@ struct DxSplit {
 
 // sum[part][i][h] (+)= sum over the part's vocabulary rows of d^T[v][i] w[v][h];
 // `rows` vocabulary rows in this piece, `piece` in the largest.
-template <int W>
+template <int W, bool ONCE>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const uint16_t* w, uint32_t ld_w, int H,
                                                                          const uint16_t* d, int64_t ldd, int rows,
                                                                          int piece, Tokens tk, float* sum,
@@ -489,7 +492,7 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : 2) void k_dx_sum(const u
   const int kt0 = (int)((int64_t)pairs * part / sp.parts) * 2, kt1 = (int)((int64_t)pairs * (part + 1) / sp.parts) * 2;
   if (kt0 == kt1) return;  // in a last piece that is shorter: nothing to add
   floatx16 acc[W][W];
-  tile_product<W, true, true, true>(TileOperand{w + m0, ld_w, H - m0, rows},
+  tile_product<W, true, true, true>(TileOperand{w + m0, ld_w, H - m0, rows, ONCE},
                               TileOperand{d + n0, (uint32_t)ldd, (int)(ldd - n0), pairs * 128}, pairs * 128, kt0, kt1, lds,
                               acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -669,20 +672,27 @@ hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
     auto allow = [](const void* f, int W) {
       if (err == hipSuccess) err = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds_of(W));
     };
-    allow(reinterpret_cast<const void*>(&k_logits_stats<4, true>), 4);
-    allow(reinterpret_cast<const void*>(&k_logits_stats<4, false>), 4);
-    allow(reinterpret_cast<const void*>(&k_logits_stats<2, true>), 2);
-    allow(reinterpret_cast<const void*>(&k_logits_stats<2, false>), 2);
-    allow(reinterpret_cast<const void*>(&k_logits_grad<4, true>), 4);
-    allow(reinterpret_cast<const void*>(&k_logits_grad<4, false>), 4);
-    allow(reinterpret_cast<const void*>(&k_logits_grad<2, true>), 2);
-    allow(reinterpret_cast<const void*>(&k_logits_grad<2, false>), 2);
-    allow(reinterpret_cast<const void*>(&k_dw<4, false, uint16_t>), 4);
-    allow(reinterpret_cast<const void*>(&k_dw<4, false, float>), 4);
-    allow(reinterpret_cast<const void*>(&k_dw<2, false, uint16_t>), 2);
-    allow(reinterpret_cast<const void*>(&k_dw<2, false, float>), 2);
-    allow(reinterpret_cast<const void*>(&k_dx_sum<4>), 4);
-    allow(reinterpret_cast<const void*>(&k_dx_sum<2>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<4, true, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<4, false, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, true, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, false, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, true, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_stats<2, false, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<4, true, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<4, false, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, true, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, false, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, true, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_logits_grad<2, false, true>), 2);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, false, uint16_t>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, false, float>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, true, uint16_t>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<4, false, true, float>), 4);
+    allow(reinterpret_cast<const void*>(&k_dw<2, false, false, uint16_t>), 2);
+    allow(reinterpret_cast<const void*>(&k_dw<2, false, false, float>), 2);
+    allow(reinterpret_cast<const void*>(&k_dx_sum<4, false>), 4);
+    allow(reinterpret_cast<const void*>(&k_dx_sum<2, false>), 2);
+    allow(reinterpret_cast<const void*>(&k_dx_sum<2, true>), 2);
   });
   return err;
 }
@@ -723,8 +733,12 @@ hipError_t launch_linear_ce(int64_t T, int64_t V, int64_t H, const void* x, int6
   const int64_t tiles = tiles_of(V, w_tile);
   float2* stats = static_cast<float2*>(workspace);
   float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16(tiles * T * 8));
+  const bool big = V * H * 2 >= kStreamBytes;  // a weight that the caches do not hold
   e = with_logits_tile(w_tile, H % 128 == 0, [&](auto W, auto even) {
-    k_logits_stats<W.value, even.value><<<(unsigned)(tiles * tiles_of(T, W.value)), TILE_THREADS, lds_of(W.value), s>>>(
+    auto* kernel = &k_logits_stats<W.value, even.value, false>;
+    if constexpr (W.value < 4)
+      if (big && tiles_of(T, W.value) == 1) kernel = &k_logits_stats<W.value, even.value, true>;
+    kernel<<<(unsigned)(tiles * tiles_of(T, W.value)), TILE_THREADS, lds_of(W.value), s>>>(
         static_cast<const uint16_t*>(w), (uint32_t)ld_w, (int)V, static_cast<const uint16_t*>(x), (uint32_t)ld_x, (int)T,
         (int)H, labels, stats, zlab);
   });
@@ -761,31 +775,41 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     k_gather<<<(unsigned)up128(T), 256, 0, s>>>(xp, ld_x, H, tk, xc);
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  // what the caches do not hold: the weight, its gradient
+  const bool big = V * H * 2 >= kStreamBytes, stream = V * H * (dw_dt == 0 ? 2 : 4) >= kStreamBytes;
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
     const int64_t n = std::min(pl.piece, V - v0);
     const uint16_t* wp = static_cast<const uint16_t*>(w) + v0 * ld_w;
     e = with_logits_tile(logits_w(T, n, H), H % 128 == 0, [&](auto W, auto even) {
       // up to 64 tokens are all in the first tile, in two parts
       const int64_t tt = T <= 64 ? 1 : tiles_of(up128(T), W.value), tv = tiles_of(up128(n), W.value);
-      k_logits_grad<W.value, even.value><<<(unsigned)(tt * tv), TILE_THREADS, lds_of(W.value), s>>>(
+      auto* kernel = &k_logits_grad<W.value, even.value, false>;
+      if constexpr (W.value < 4)
+        if (big && tiles_of(T, W.value) == 1) kernel = &k_logits_grad<W.value, even.value, true>;
+      kernel<<<(unsigned)(tt * tv), TILE_THREADS, lds_of(W.value), s>>>(
           wp, (uint32_t)ld_w, (int)n, xc, (int)H, (int)tt, v0, tk, labels, lse, dloss, d, pl.ldd);
     });
     if (e != hipSuccess) return e;
     if (dw != nullptr) {
       uint8_t* out = static_cast<uint8_t*>(dw) + v0 * ld_dw * (dw_dt == 0 ? 2 : 4);
       if (T <= FEW_DW_TOKENS) {
-        e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, s);
+        e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, stream, s);
       } else {
         auto go = [&](auto W, auto with_short) {
           constexpr bool SHORT = with_short.value;
           const unsigned grid = (unsigned)(tiles_of(H, W.value) * tiles_of(n, W.value));
           const int lds = SHORT ? tile_lds(W.value) / 2 : lds_of(W.value);
+          auto run = [&](auto* o) {
+            using OutT = std::remove_pointer_t<decltype(o)>;
+            auto* kernel = &k_dw<W.value, SHORT, false, OutT>;
+            if constexpr (W.value == 4 || SHORT)
+              if (stream) kernel = &k_dw<W.value, SHORT, true, OutT>;
+            kernel<<<grid, TILE_THREADS, lds, s>>>(xc, (int)H, d, pl.ldd, (int)n, tk, o, ld_dw, accumulate);
+          };
           if (dw_dt == 0)
-            k_dw<W.value, SHORT><<<grid, TILE_THREADS, lds, s>>>(
-                xc, (int)H, d, pl.ldd, (int)n, tk, reinterpret_cast<uint16_t*>(out), ld_dw, accumulate);
+            run(reinterpret_cast<uint16_t*>(out));
           else
-            k_dw<W.value, SHORT><<<grid, TILE_THREADS, lds, s>>>(
-                xc, (int)H, d, pl.ldd, (int)n, tk, reinterpret_cast<float*>(out), ld_dw, accumulate);
+            run(reinterpret_cast<float*>(out));
           return hipGetLastError();
         };
         using std::integral_constant;
@@ -800,7 +824,10 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     }
     if (dx != nullptr) {
       e = with_tile(pl.dxp.W, true, [&](auto W, auto) {
-        k_dx_sum<W.value><<<(unsigned)pl.dxp.units, TILE_THREADS, lds_of(W.value), s>>>(
+        auto* kernel = &k_dx_sum<W.value, false>;
+        if constexpr (W.value < 4)
+          if (big && tiles_of(T, W.value) == 1) kernel = &k_dx_sum<W.value, true>;
+        kernel<<<(unsigned)pl.dxp.units, TILE_THREADS, lds_of(W.value), s>>>(
             wp, (uint32_t)ld_w, (int)H, d, pl.ldd, (int)n, (int)pl.piece, tk, sum, v0 > 0 ? 1 : 0);
       });
       if (e != hipSuccess) return e;

@@ -10,8 +10,9 @@
 // all lanes, makes the operand of one matrix instruction, whose column i stands for
 // column 8 i + j of the wave's 128.  A lane then ends up with 8 adjacent columns of
 // a row of dw, one 16-byte store.
-// 131072 x 5120 BF16: 0.25 ms at 16 tokens (5.4 TB/s; a plain store loop reaches
-// 5.3) and 0.32 at 64, against 0.35 and more for the tiles.
+// 131072 x 5120 BF16: 0.28 ms at 16 tokens in two parts (4.8 TB/s; a plain store loop
+// reaches 5.3).  From 33 tokens on the tiles are level or better (47 x 16555 x 2264
+// 64 us in all against 53).
 #include <algorithm>
 
 #include "layers_launch.hpp"
@@ -39,7 +40,7 @@ __device__ __forceinline__ bf16x8_t block_column(const uint32_t (&rows)[8][C / 2
 // A wave holds 32 KT rows (tokens, in two parts) of C columns per lane (128 columns in all) of xc in
 // registers and walks the vocabulary 16 rows at a time; the four waves take
 // adjacent columns of the same rows.
-template <int KT, typename OutT>
+template <int KT, bool STREAM, typename OutT>
 __global__ __launch_bounds__(256) void k_few_dw(const uint16_t* xc, int H, const uint16_t* dt, int64_t ldt, int rows,
                                                 int slices, int parts, Tokens tk, OutT* dw, int64_t ld_dw,
                                                 int accumulate) {
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(256) void k_few_dw(const uint16_t* xc, int H, const
             const float4 old = *p;
             s = make_float4(old.x + s.x, old.y + s.y, old.z + s.z, old.w + s.w);
           }
-          *p = s;
+          store16<STREAM>(p, __builtin_bit_cast(u32x4_t, s));
         }
       } else {
         uint32_t* p = reinterpret_cast<uint32_t*>(o);
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(256) void k_few_dw(const uint16_t* xc, int H, const
         }
 #pragma unroll
         for (int j = 0; j < C / 2; j++) b[j] = bf16_pack(f[2 * j], f[2 * j + 1]);
-        *reinterpret_cast<u32x4_t*>(p) = u32x4_t{b[0], b[1], b[2], b[3]};
+        store16<STREAM>(p, u32x4_t{b[0], b[1], b[2], b[3]});
       }
     }
 #pragma unroll
@@ -137,27 +138,26 @@ constexpr int64_t kStreams = 1024;
 
 template <typename OutT>
 static hipError_t few_dw_t(const uint16_t* xc, int64_t H, const uint16_t* dt, int64_t ldt, int64_t rows, int64_t T,
-                           Tokens tk, OutT* dw, int64_t ld_dw, int accumulate, hipStream_t s) {
+                           Tokens tk, OutT* dw, int64_t ld_dw, int accumulate, bool stream, hipStream_t s) {
   auto go = [&](auto kt) {
     const int64_t slices = (H + 64 * C - 1) / (64 * C), groups = (rows + 15) / 16;
     const int64_t parts = std::max<int64_t>(1, std::min((2 * kStreams + slices - 1) / slices, groups / 4));
-    k_few_dw<kt.value><<<(unsigned)(slices * parts), 256, 0, s>>>(
-        xc, (int)H, dt, ldt, (int)rows, (int)slices, (int)parts, tk, dw, ld_dw, accumulate);
+    auto* kernel = stream ? &k_few_dw<kt.value, true, OutT> : &k_few_dw<kt.value, false, OutT>;
+    kernel<<<(unsigned)(slices * parts), 256, 0, s>>>(xc, (int)H, dt, ldt, (int)rows, (int)slices, (int)parts, tk, dw,
+                                                      ld_dw, accumulate);
   };
   using std::integral_constant;
   if (T <= 16)
     go(integral_constant<int, 1>{});
-  else if (T <= 32)
-    go(integral_constant<int, 2>{});
   else
-    go(integral_constant<int, 4>{});
+    go(integral_constant<int, 2>{});
   return hipGetLastError();
 }
 
 hipError_t few_dw(const uint16_t* xc, int64_t H, const uint16_t* dt, int64_t ldt, int64_t rows, int64_t T, Tokens tk,
-                  void* dw, int dw_f32, int64_t ld_dw, int accumulate, hipStream_t s) {
-  if (dw_f32) return few_dw_t(xc, H, dt, ldt, rows, T, tk, static_cast<float*>(dw), ld_dw, accumulate, s);
-  return few_dw_t(xc, H, dt, ldt, rows, T, tk, static_cast<uint16_t*>(dw), ld_dw, accumulate, s);
+                  void* dw, int dw_f32, int64_t ld_dw, int accumulate, bool stream, hipStream_t s) {
+  if (dw_f32) return few_dw_t(xc, H, dt, ldt, rows, T, tk, static_cast<float*>(dw), ld_dw, accumulate, stream, s);
+  return few_dw_t(xc, H, dt, ldt, rows, T, tk, static_cast<uint16_t*>(dw), ld_dw, accumulate, stream, s);
 }
 
 }  // namespace nvfp4

@@ -593,10 +593,6 @@ void with_vpt(int vpt, F&& f) {
   }
 }
 
-// Bytes from which on a launch streams past the caches (256 MB hold little of it
-// until the next reader comes).
-constexpr int64_t kStreamBytes = int64_t(128) << 20;
-
 template <typename T>
 hipError_t dropout_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x, void* y, int64_t ld_y, const Dropout& d,
                      hipStream_t s) {

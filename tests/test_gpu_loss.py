@@ -216,6 +216,21 @@ def test_weight_rows_that_span_more_than_32_bits():
     q.check_dw(dw, BF)
 
 
+@pytest.mark.parametrize("T,dw_dt,beta", [(3, BF, 0.0), (20, F32, 1.0), (60, BF, 1.0), (120, F32, 0.0), (300, BF, 0.0), (300, F32, 1.0),
+                                          (1700, BF, 1.0)])
+def test_weights_larger_than_the_caches(T, dw_dt, beta):
+    """143 MB of weight, whose loads and gradient stores take other ways past the caches."""
+    q = Head(T, 70001, 1024, 0.1, seed=13).reference()
+    loss, lse = q.forward()
+    q.check_forward(loss, lse)
+    dw0 = None
+    if beta:
+        dw0 = (q.torch.randn(q.V, q.H, device="cuda") * 0.01).to(q.torch.bfloat16 if dw_dt == BF else q.torch.float32)
+    dx, dw = q.backward(lse, dw_dt, beta, dw0=dw0)
+    q.check_dx(dx)
+    q.check_dw(dw, dw_dt, dw0)
+
+
 @pytest.mark.parametrize("T", [1, 20, 90, 300])
 @pytest.mark.parametrize("dw_dt", [BF, F32])
 def test_accumulated_weight_gradient_and_single_outputs(T, dw_dt):
