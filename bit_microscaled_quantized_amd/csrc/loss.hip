@@ -663,6 +663,13 @@ BackPlan back_plan(int64_t T, int64_t V, int64_t H) {
   return p;
 }
 
+// Whether a weight that one tile of tokens reads passes the caches by: one that they
+// do not hold, in rows of whole 128-byte lines (others' lines serve two stages: 3 x
+// 55044 x 3568 86 us through the caches, 101 past them).
+bool passes_once(const void* w, int64_t ld_w, int64_t V, int64_t H) {
+  return V * H * 2 >= kStreamBytes && ld_w % 64 == 0 && reinterpret_cast<uintptr_t>(w) % 128 == 0;
+}
+
 // Dynamic LDS of a tile kernel: its stages and the token values of a tile.
 constexpr int lds_of(int W) { return tile_lds(W) + 3 * tile_side(W) * 4; }
 hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
@@ -733,11 +740,11 @@ hipError_t launch_linear_ce(int64_t T, int64_t V, int64_t H, const void* x, int6
   const int64_t tiles = tiles_of(V, w_tile);
   float2* stats = static_cast<float2*>(workspace);
   float* zlab = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + up16(tiles * T * 8));
-  const bool big = V * H * 2 >= kStreamBytes;  // a weight that the caches do not hold
+  const bool once = passes_once(w, ld_w, V, H);
   e = with_logits_tile(w_tile, H % 128 == 0, [&](auto W, auto even) {
     auto* kernel = &k_logits_stats<W.value, even.value, false>;
     if constexpr (W.value < 4)
-      if (big && tiles_of(T, W.value) == 1) kernel = &k_logits_stats<W.value, even.value, true>;
+      if (once && tiles_of(T, W.value) == 1) kernel = &k_logits_stats<W.value, even.value, true>;
     kernel<<<(unsigned)(tiles * tiles_of(T, W.value)), TILE_THREADS, lds_of(W.value), s>>>(
         static_cast<const uint16_t*>(w), (uint32_t)ld_w, (int)V, static_cast<const uint16_t*>(x), (uint32_t)ld_x, (int)T,
         (int)H, labels, stats, zlab);
@@ -775,8 +782,8 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     k_gather<<<(unsigned)up128(T), 256, 0, s>>>(xp, ld_x, H, tk, xc);
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  // what the caches do not hold: the weight, its gradient
-  const bool big = V * H * 2 >= kStreamBytes, stream = V * H * (dw_dt == 0 ? 2 : 4) >= kStreamBytes;
+  // a gradient that the caches do not hold
+  const bool once = passes_once(w, ld_w, V, H), stream = V * H * (dw_dt == 0 ? 2 : 4) >= kStreamBytes;
   for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
     const int64_t n = std::min(pl.piece, V - v0);
     const uint16_t* wp = static_cast<const uint16_t*>(w) + v0 * ld_w;
@@ -785,7 +792,7 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
       const int64_t tt = T <= 64 ? 1 : tiles_of(up128(T), W.value), tv = tiles_of(up128(n), W.value);
       auto* kernel = &k_logits_grad<W.value, even.value, false>;
       if constexpr (W.value < 4)
-        if (big && tiles_of(T, W.value) == 1) kernel = &k_logits_grad<W.value, even.value, true>;
+        if (once && tiles_of(T, W.value) == 1) kernel = &k_logits_grad<W.value, even.value, true>;
       kernel<<<(unsigned)(tt * tv), TILE_THREADS, lds_of(W.value), s>>>(
           wp, (uint32_t)ld_w, (int)n, xc, (int)H, (int)tt, v0, tk, labels, lse, dloss, d, pl.ldd);
     });
@@ -793,7 +800,9 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
     if (dw != nullptr) {
       uint8_t* out = static_cast<uint8_t*>(dw) + v0 * ld_dw * (dw_dt == 0 ? 2 : 4);
       if (T <= FEW_DW_TOKENS) {
-        e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, stream, s);
+        // past the caches in whole 128-byte lines only (2 x 116087 x 1720: 248 us for d and dw, 283 past them)
+        const bool lines = ld_dw * (dw_dt == 0 ? 2 : 4) % 128 == 0 && reinterpret_cast<uintptr_t>(dw) % 128 == 0;
+        e = few_dw(xc, H, d, pl.ldd, n, T, tk, out, dw_dt, ld_dw, accumulate, stream && lines, s);
       } else {
         auto go = [&](auto W, auto with_short) {
           constexpr bool SHORT = with_short.value;
@@ -826,7 +835,7 @@ hipError_t launch_linear_ce_back(int64_t T, int64_t V, int64_t H, const void* x,
       e = with_tile(pl.dxp.W, true, [&](auto W, auto) {
         auto* kernel = &k_dx_sum<W.value, false>;
         if constexpr (W.value < 4)
-          if (big && tiles_of(T, W.value) == 1) kernel = &k_dx_sum<W.value, true>;
+          if (once && tiles_of(T, W.value) == 1) kernel = &k_dx_sum<W.value, true>;
         kernel<<<(unsigned)pl.dxp.units, TILE_THREADS, lds_of(W.value), s>>>(
             wp, (uint32_t)ld_w, (int)H, d, pl.ldd, (int)n, (int)pl.piece, tk, sum, v0 > 0 ? 1 : 0);
       });
