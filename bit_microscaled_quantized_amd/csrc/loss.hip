@@ -614,9 +614,10 @@ int logits_w(int64_t M, int64_t N, int64_t K) {
 }
 
 // Up to here the dw product has few enough stages that four small tiles per CU,
-// each unpipelined, beat one large tile, where there are that many (131072 x 5120: 0.63 against 0.76 ms at 256
-// tokens, 1.49 against 1.59 at 1000, 2.75 against 2.61 at 2000).
-constexpr int64_t SHORT_DW_TOKENS = 1536;
+// each unpipelined, beat one large tile, where there are that many (131072 x 5120, d
+// and dw: 0.86 against 0.97 ms at 256 tokens, 1.91 against 1.85 at 600, 2.77 against
+// 2.53 at 1000; 30000 x 2048: 0.089 against 0.103 at 256, level at 1000).
+constexpr int64_t SHORT_DW_TOKENS = 512;
 
 // Workgroups of the dx product: its tiles are as few as T x H gives, so K (a
 // piece's vocabulary rows) is split, by the rounds that cost least.

@@ -562,7 +562,7 @@ __global__ __launch_bounds__(DG * 32) void k_dgamma(const float* partial, uint32
 
 // A backward pass keeps about two workgroups of 640 lanes on each CU of a 256-CU
 // MI355X, or one of up to 1024 for wider rows: more of them write more partial
-// sums than their overlap gains (8192 x 5120: 92 us at 512 workgroups, 115 at 1024).
+// sums than their overlap gains (8192 x 5120, before loads went ahead: 92 us at 512 workgroups, 115 at 1024).
 constexpr int64_t kCus = 256;
 constexpr int kBackThreads = 640;
 
@@ -646,10 +646,13 @@ hipError_t norm_t(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Rows that a group of lanes takes in turn where one workgroup does the whole pass:
+// more take longer than a second launch (8 x 2048, two each: 7.5 us against 7.7 in
+// two launches; 4 x 5120, four: 10.0 against 8.2).
+constexpr int kAloneRows = 2;
+
 // Shape of a backward pass of vectors of N elements: rows (groups of G lanes) per
 // workgroup, and workgroups, each with one row of partial sums.
-// rows a group of lanes takes in turn there (8 x 2048: 7.5 us against 7.7 in two launches, 4 x 5120 10.0 against 8.2)
-constexpr int kAloneRows = 2;
 struct BackShape {
   RowShape row;
   int groups;
