@@ -207,17 +207,21 @@ def linear_cross_entropy(x, w, labels):
 
 
 class AddRMSNorm(torch.nn.Module):
-    """add_rms_norm with its gain; dropout draws a new mask every training call,
-    reproducibly from the module's seed."""
+    """add_rms_norm with its gain.  In training, dropout takes a new mask every call: its
+    seed is a draw from torch's CPU generator, mixed with the module's seed (for modules,
+    or ranks, whose generators run alike).  So torch.manual_seed repeats a run's masks,
+    the generator's saved state resumes them, and torch.utils.checkpoint, which restores
+    that state, recomputes a forward pass with the mask it had."""
 
     def __init__(self, features: int, eps: float = 1e-5, p: float = 0.0, seed: int = 0, device="cuda", dtype=None):
         super().__init__()
         self.gamma = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype or torch.bfloat16))
-        self.eps, self.p, self.seed, self.calls = eps, p, seed, 0
+        self.eps, self.p, self.seed = eps, p, seed
 
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:
             return add_rms_norm(x, residual, self.gamma, self.eps)
-        s = (self.seed << 32) + self.calls
-        self.calls += 1
+        draw = int(torch.randint(2 ** 63 - 1, (), dtype=torch.int64, device="cpu"))
+        # an odd factor: different seeds below 2^64 stay different
+        s = (draw ^ self.seed * 0x9E3779B97F4A7C15) & (2 ** 64 - 1)
         return add_rms_norm(x, residual, self.gamma, self.eps, self.p, s)

@@ -212,3 +212,28 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for b, w, name in zip((one, two), want, "ab"):
         _same(torch, b, w, f"stream {name}")
+
+
+@pytest.mark.parametrize("use_reentrant", [False, True])
+def test_checkpointed_norm_with_dropout(use_reentrant):
+    """Activation checkpointing gives the bytes of the step without it, dropout's mask included."""
+    torch = gpuio.torch_cuda()
+    from torch.utils.checkpoint import checkpoint
+    from bit_microscaled_quantized_amd.layers import AddRMSNorm
+    g = torch.Generator(device="cuda").manual_seed(4)
+    data = [torch.randn(40, 264, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    module = AddRMSNorm(264, p=0.3, seed=1)
+
+    def branch(a, b):
+        h, y = module(torch.tanh(a), b)
+        return h.float().sum() + y.float().square().sum()
+    grads = []
+    for through in (lambda f, *a: f(*a), lambda f, *a: checkpoint(f, *a, use_reentrant=use_reentrant)):
+        torch.manual_seed(7)
+        module.zero_grad()
+        x, r = (t.clone().requires_grad_() for t in data)
+        through(branch, x, r).backward()
+        grads.append((x.grad, r.grad, module.gamma.grad.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    dropped = grads[0][0] == 0
+    assert 0.2 < float(dropped.float().mean()) < 0.4

@@ -1,0 +1,119 @@
+"""The autograd layer's own arithmetic on the host: a stand-in written in elementary torch
+operations takes the place of the kernels, so that seeds, shapes and refusals of
+bit_microscaled_quantized_amd.layers are tested without a device."""
+import copy
+
+import pytest
+import torch
+from torch.utils.checkpoint import checkpoint
+
+from bit_microscaled_quantized_amd import layers
+
+COLS = 48
+
+
+def _mask(rows, cols, p, seed):
+    g = torch.Generator().manual_seed(seed % 2 ** 63)
+    return (torch.rand(rows, cols, generator=g) >= p) / (1.0 - p)
+
+
+class Kernels:
+    """nvfp4_rms_norm and its backward for packed FP32 host tensors; keeps the seeds it was given."""
+
+    def __init__(self):
+        self.seeds = []
+
+    def nvfp4_rms_norm(self, x, r, dt, rows, cols, ld_x, ld_r, gamma, gdt, eps, p, seed, h, ld_h, y, ld_y, codes, scales,
+                       rstd):
+        self.seeds.append(seed % 2 ** 64)
+        h.copy_((x * _mask(rows, cols, p, seed) + (0 if r is None else r)).view(h.shape))
+        rstd.copy_(torch.rsqrt(h.view(rows, cols).square().mean(1) + eps))
+        y.copy_((h.view(rows, cols) * rstd[:, None] * gamma).view(y.shape))
+
+    def nvfp4_rms_norm_backward_workspace_size(self, rows, cols):
+        return 0
+
+    def nvfp4_rms_norm_backward(self, dy, dh, h, dt, rows, cols, ld_dy, ld_dh, ld_h, gamma, gdt, rstd, p, seed, dx, ld_dx,
+                                dr, ld_dr, dgamma, ws):
+        n = h.view(rows, cols) * rstd[:, None]
+        gy = dy.view(rows, cols) * gamma
+        g = rstd[:, None] * (gy - n * (gy * n).mean(1, keepdim=True)) + (0 if dh is None else dh.view(rows, cols))
+        for out, v in ((dx, g * _mask(rows, cols, p, seed)), (dr, g)):
+            if out is not None:
+                out.copy_(v.view(out.shape))
+        if dgamma is not None:
+            dgamma.copy_((dy.view(rows, cols) * n).sum(0))
+
+
+@pytest.fixture
+def kernels(monkeypatch):
+    k = Kernels()
+    for name in ("nvfp4_rms_norm", "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_size"):
+        monkeypatch.setattr(layers.nv, name, getattr(k, name))
+    monkeypatch.setattr(layers, "_on_gpu", lambda *tensors: None)
+    return k
+
+
+def norm(**kw):
+    return layers.AddRMSNorm(COLS, p=0.5, device="cpu", dtype=torch.float32, **kw)
+
+
+def branch(module, x, r):
+    h, y = module(torch.tanh(x), r)
+    return (h * 0.3 + y.square()).sum()
+
+
+@pytest.mark.parametrize("use_reentrant", [False, True])
+def test_checkpointed_norm_repeats_its_mask(kernels, use_reentrant):
+    """The recomputed forward has to draw the mask of the first one: gradients are those
+    without checkpointing, bit for bit."""
+    module = norm(seed=3)
+    g = torch.Generator().manual_seed(1)
+    data = [torch.randn(6, COLS, generator=g) for _ in range(2)]
+    grads = []
+    for through in (lambda f, *a: f(*a), lambda f, *a: checkpoint(f, *a, use_reentrant=use_reentrant)):
+        torch.manual_seed(7)
+        x, r = (t.clone().requires_grad_() for t in data)
+        m = copy.deepcopy(module)
+        through(lambda a, b: branch(m, a, b), x, r).backward()
+        grads.append((x.grad, r.grad, m.gamma.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    assert len(kernels.seeds) == 3 and len(set(kernels.seeds)) == 1
+
+
+def test_every_norm_and_call_has_a_mask_of_its_own(kernels):
+    """Modules built alike, and the calls of one module, drop different elements; modules
+    that differ in their seed do too where torch's generator stands at the same state."""
+    x = torch.randn(2, COLS)
+    a, b = norm(), norm()
+    for _ in range(3):
+        for m in (a, b):
+            m(x)
+    torch.manual_seed(5)
+    norm(seed=1)(x)
+    torch.manual_seed(5)
+    norm(seed=2)(x)
+    assert len(set(kernels.seeds)) == 8, kernels.seeds
+
+
+def test_a_resumed_run_continues_its_masks(kernels):
+    """The parameters and torch's generator state, saved and restored, are all it takes."""
+    x = torch.randn(2, COLS)
+    torch.manual_seed(11)
+    m = norm(seed=4)
+    m(x)
+    saved, rng = copy.deepcopy(m.state_dict()), torch.get_rng_state()
+    m(x)
+    other = norm(seed=4)
+    other.load_state_dict(saved)
+    torch.manual_seed(0)
+    torch.set_rng_state(rng)
+    other(x)
+    assert kernels.seeds[2] == kernels.seeds[1] != kernels.seeds[0]
+
+
+def test_evaluation_draws_nothing(kernels):
+    m = norm(seed=1).eval()
+    rng = torch.get_rng_state()
+    h, _ = m(torch.ones(2, COLS))
+    assert torch.equal(h, torch.ones(2, COLS)) and torch.equal(torch.get_rng_state(), rng)
