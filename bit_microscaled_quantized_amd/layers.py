@@ -206,12 +206,18 @@ def linear_cross_entropy(x, w, labels):
     return token_cross_entropy(x, w, labels).sum() / valid.sum().clamp(min=1)
 
 
+def _capturing(x) -> bool:
+    return x.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 class AddRMSNorm(torch.nn.Module):
     """add_rms_norm with its gain.  In training, dropout takes a new mask every call: its
     seed is a draw from torch's CPU generator, mixed with the module's seed (for modules,
     or ranks, whose generators run alike).  So torch.manual_seed repeats a run's masks,
     the generator's saved state resumes them, and torch.utils.checkpoint, which restores
-    that state, recomputes a forward pass with the mask it had."""
+    that state, recomputes a forward pass with the mask it had.  A launch's seed is its
+    argument, so every replay of a captured graph would drop the same elements: under
+    capture dropout is refused."""
 
     def __init__(self, features: int, eps: float = 1e-5, p: float = 0.0, seed: int = 0, device="cuda", dtype=None):
         super().__init__()
@@ -221,6 +227,9 @@ class AddRMSNorm(torch.nn.Module):
     def forward(self, x, residual=None):
         if not self.training or self.p == 0.0:
             return add_rms_norm(x, residual, self.gamma, self.eps)
+        if _capturing(x):
+            raise RuntimeError("AddRMSNorm draws a new dropout mask every call, and a captured graph would replay "
+                               "one: capture it with p = 0, or add_rms_norm with a seed of your own")
         draw = int(torch.randint(2 ** 63 - 1, (), dtype=torch.int64, device="cpu"))
         # an odd factor: different seeds below 2^64 stay different
         s = (draw ^ self.seed * 0x9E3779B97F4A7C15) & (2 ** 64 - 1)

@@ -237,3 +237,22 @@ def test_checkpointed_norm_with_dropout(use_reentrant):
     assert all(torch.equal(a, b) for a, b in zip(*grads))
     dropped = grads[0][0] == 0
     assert 0.2 < float(dropped.float().mean()) < 0.4
+
+
+def test_captured_module_refuses_dropout():
+    """A graph would replay one mask; p = 0 and a seed of the caller's are captured."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import AddRMSNorm, add_rms_norm
+    x = torch.randn(3, 64, device="cuda").bfloat16()
+    module = AddRMSNorm(64, p=0.3)
+    with torch.no_grad():
+        want = add_rms_norm(x, None, module.gamma, p=0.3, seed=5)[1]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            with pytest.raises(RuntimeError, match="captured graph"):
+                module(x)
+            got = add_rms_norm(x, None, module.gamma, p=0.3, seed=5)[1]
+            kept = module.eval()(x)[0]
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(kept, x)

@@ -117,3 +117,16 @@ def test_evaluation_draws_nothing(kernels):
     rng = torch.get_rng_state()
     h, _ = m(torch.ones(2, COLS))
     assert torch.equal(h, torch.ones(2, COLS)) and torch.equal(torch.get_rng_state(), rng)
+
+
+def test_a_captured_call_would_repeat_one_mask_and_is_refused(kernels, monkeypatch):
+    """A launch's seed is its argument: every replay would drop what the capture dropped.
+    Without dropout, and with a seed that the caller gives, there is nothing to refuse."""
+    monkeypatch.setattr(layers, "_capturing", lambda x: True)
+    m, x = norm(seed=1), torch.ones(2, COLS)
+    with pytest.raises(RuntimeError, match="capture"):
+        m(x)
+    assert kernels.seeds == []
+    layers.add_rms_norm(x, None, m.gamma, p=0.5, seed=9)
+    m.eval()(x)
+    assert kernels.seeds == [9, 0]
