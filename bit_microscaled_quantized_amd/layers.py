@@ -30,10 +30,13 @@ def _dt(t) -> int:
 
 
 def _on_gpu(x, *others):
-    """Refuses host tensors, and tensors on another device than x's: the kernels take
-    addresses."""
+    """Refuses host tensors, and tensors on another device than the current one: the
+    kernels take addresses, and run on the current device's stream."""
     if not x.is_cuda:
         raise ValueError(f"expected tensors on the GPU, got one on {x.device}")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"expected tensors on the current device, cuda:{torch.cuda.current_device()}, got one on "
+                         f"{x.device}")
     for t in others:
         if t is not None and t.device != x.device:
             raise ValueError(f"expected tensors on {x.device}, got one on {t.device}")

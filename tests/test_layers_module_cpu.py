@@ -130,3 +130,22 @@ def test_a_captured_call_would_repeat_one_mask_and_is_refused(kernels, monkeypat
     layers.add_rms_norm(x, None, m.gamma, p=0.5, seed=9)
     m.eval()(x)
     assert kernels.seeds == [9, 0]
+
+
+class OnDevice:
+    """What the device checks look at of a tensor on GPU `index`."""
+    is_cuda = True
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    """The kernels are launched on the current device, on its stream."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    layers._on_gpu(OnDevice(0), OnDevice(0), None)
+    for tensors in ((OnDevice(1),), (OnDevice(1), OnDevice(1)), (OnDevice(0), OnDevice(1))):
+        with pytest.raises(ValueError, match="cuda:"):
+            layers._on_gpu(*tensors)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    layers._on_gpu(OnDevice(1), OnDevice(1))
