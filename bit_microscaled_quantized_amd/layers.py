@@ -20,6 +20,7 @@ from torch.autograd.function import once_differentiable
 
 from . import nvfp4 as nv
 
+_on_gpu = nv.on_current_device
 _DT = {torch.bfloat16: nv.NVFP4_BF16, torch.float32: nv.NVFP4_F32}
 
 
@@ -27,19 +28,6 @@ def _dt(t) -> int:
     if t.dtype not in _DT:
         raise TypeError(f"expected a bfloat16 or float32 tensor, got {t.dtype}")
     return _DT[t.dtype]
-
-
-def _on_gpu(x, *others):
-    """Refuses host tensors, and tensors on another device than the current one: the
-    kernels take addresses, and run on the current device's stream."""
-    if not x.is_cuda:
-        raise ValueError(f"expected tensors on the GPU, got one on {x.device}")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"expected tensors on the current device, cuda:{torch.cuda.current_device()}, got one on "
-                         f"{x.device}")
-    for t in others:
-        if t is not None and t.device != x.device:
-            raise ValueError(f"expected tensors on {x.device}, got one on {t.device}")
 
 
 def _norm_args(x, residual, gamma):

@@ -76,6 +76,7 @@ def _function():
     class NVFP4LinearFn(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, w, sign_mask: int, seed_row: int, seed_col: int):
+            nv.on_current_device(x, w)
             dev = x.device
             IN = x.shape[-1]
             OUT = w.shape[0]

@@ -137,6 +137,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def on_current_device(*tensors):
+    """Refuses host tensors, and tensors on another device than the current one (None is
+    none): the kernels take addresses, and run on the current device's stream."""
+    import torch
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"expected tensors on the GPU, got one on {t.device}")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"expected tensors on the current device, cuda:{torch.cuda.current_device()}, got one "
+                             f"on {t.device}")
+
+
 def nvfp4_status_str(status: int) -> str:
     return load_library().nvfp4_status_str(status).decode()
 
