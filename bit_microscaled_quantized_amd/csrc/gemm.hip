@@ -60,6 +60,7 @@
 #include "gemm_tiling.hpp"
 #include "nvfp4_device.hpp"
 #include "nvfp4_launch.hpp"
+#include "per_device.hpp"
 
 namespace nvfp4 {
 
@@ -523,11 +524,10 @@ hipError_t launch_gemm_t(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes
                          const uint8_t* b_scales, int b_rowdiv, const float* b_ts, OutT* c,
                          int64_t ldc, int accumulate, void* workspace, int64_t workspace_bytes,
                          hipStream_t s) {
-  static std::once_flag once;
-  static hipError_t attr_err = hipSuccess;
-  std::call_once(once, [] {
-    attr_err = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_nvfp4<OutT>),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+  static std::atomic<uint64_t> lds_allowed{0};
+  const hipError_t attr_err = once_per_device(lds_allowed, [] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_nvfp4<OutT>),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
   });
   if (attr_err != hipSuccess) return attr_err;
   SplitPlan p = plan_split(M, N, K);

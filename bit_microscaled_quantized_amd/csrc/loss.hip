@@ -20,8 +20,7 @@
 #include "bf16_tile.hpp"
 #include "layers_launch.hpp"
 #include "loss_device.hpp"
-
-#include <mutex>
+#include "per_device.hpp"
 
 namespace nvfp4 {
 
@@ -673,11 +672,11 @@ bool passes_once(const void* w, int64_t ld_w, int64_t V, int64_t H) {
 
 // Dynamic LDS of a tile kernel: its stages and the token values of a tile.
 constexpr int lds_of(int W) { return tile_lds(W) + 3 * tile_side(W) * 4; }
-hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
-  static std::once_flag once;
-  static hipError_t err = hipSuccess;
-  std::call_once(once, [] {
-    auto allow = [](const void* f, int W) {
+hipError_t allow_lds() {  // beyond 64 KB a kernel has to be told
+  static std::atomic<uint64_t> done{0};
+  return once_per_device(done, [] {
+    hipError_t err = hipSuccess;
+    auto allow = [&err](const void* f, int W) {
       if (err == hipSuccess) err = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds_of(W));
     };
     allow(reinterpret_cast<const void*>(&k_logits_stats<4, true, false>), 4);
@@ -701,8 +700,8 @@ hipError_t allow_lds() {  // once: beyond 64 KB a kernel has to be told
     allow(reinterpret_cast<const void*>(&k_dx_sum<4, false>), 4);
     allow(reinterpret_cast<const void*>(&k_dx_sum<2, false>), 2);
     allow(reinterpret_cast<const void*>(&k_dx_sum<2, true>), 2);
+    return err;
   });
-  return err;
 }
 
 // f(W, EVEN) with the tile size, and whether K is a whole number of pairs of

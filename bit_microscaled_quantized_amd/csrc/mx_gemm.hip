@@ -19,11 +19,10 @@
 // summary), Resumo tecnico, parts 1 and 2 (MXFP4, the format NVFP4 is
 // compared with: 32-element blocks, power-of-two UE8M0 scales, no tensor
 // scale).
-#include <mutex>
-
 #include "gemm_tiling.hpp"
 #include "nvfp4_device.hpp"
 #include "nvfp4_launch.hpp"
+#include "per_device.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -260,11 +259,10 @@ hipError_t launch_mx_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a_code
                           const uint8_t* a_scales, const uint8_t* b_codes, const uint8_t* b_scales,
                           float* c, int64_t ldc, int accumulate, void* workspace,
                           int64_t workspace_bytes, hipStream_t s) {
-  static std::once_flag once;
-  static hipError_t attr_err = hipSuccess;
-  std::call_once(once, [] {
-    attr_err = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_mxfp4),
-                                   hipFuncAttributeMaxDynamicSharedMemorySize, MX_LDS_BYTES);
+  static std::atomic<uint64_t> lds_allowed{0};
+  const hipError_t attr_err = once_per_device(lds_allowed, [] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_mxfp4),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, MX_LDS_BYTES);
   });
   if (attr_err != hipSuccess) return attr_err;
   SplitPlan p = plan_split(M, N, K);
