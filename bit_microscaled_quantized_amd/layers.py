@@ -52,6 +52,15 @@ def _rows(t):
     return m, max(m.stride(0), m.shape[1])
 
 
+def _operand(t):
+    """_rows as the cross entropy takes them, 16-byte rows less than 2^22 elements apart:
+    other slices are copied."""
+    m, ld = _rows(t)
+    if ld % 8 or ld >= 2 ** 22 or m.data_ptr() % 16:
+        m, ld = m.contiguous(), m.shape[1]
+    return m, ld
+
+
 class _Dropout(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, seed):
@@ -150,15 +159,10 @@ class _LinearCrossEntropy(torch.autograd.Function):
             raise ValueError("expected x [..., H], weight [V, H] and one label per token")
         if labels.is_floating_point() or labels.is_complex():
             raise TypeError(f"expected integer labels, got {labels.dtype}")
-        m, ld = _rows(x)
+        m, ld = _operand(x)
+        wc, ld_w = _operand(w)
         T, H = m.shape
         V = w.shape[0]
-        # 16-byte rows: slices that break them are copied
-        if ld % 8 or m.data_ptr() % 16:
-            m, ld = m.contiguous(), H
-        wc, ld_w = _rows(w)
-        if ld_w % 8 or wc.data_ptr() % 16:
-            wc, ld_w = wc.contiguous(), H
         y = labels.reshape(-1).to(torch.int64).contiguous()
         loss = torch.empty(T, dtype=torch.float32, device=m.device)
         lse = torch.empty_like(loss)

@@ -256,3 +256,19 @@ def test_captured_module_refuses_dropout():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(kept, x)
+
+
+def test_loss_of_the_last_tokens_of_long_sequences():
+    """Hidden states a whole sequence apart, more than 2^22 elements: value and gradient of
+    the packed rows."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import linear_cross_entropy
+    g = torch.Generator(device="cuda").manual_seed(6)
+    hidden = torch.randn(3, 2100, 2048, generator=g, device="cuda").bfloat16().requires_grad_()
+    w = (torch.randn(300, 2048, generator=g, device="cuda") * 0.02).bfloat16()
+    y = torch.tensor([5, 299, -100], device="cuda")
+    packed = hidden.detach()[:, -1].clone().requires_grad_()
+    linear_cross_entropy(hidden[:, -1], w, y).backward()
+    linear_cross_entropy(packed, w, y).backward()
+    assert torch.equal(hidden.grad[:, -1], packed.grad) and bool((packed.grad[:2] != 0).any())
+    assert bool((hidden.grad[:, :-1] == 0).all())

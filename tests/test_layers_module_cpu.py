@@ -149,3 +149,49 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch)
             layers._on_gpu(*tensors)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     layers._on_gpu(OnDevice(1), OnDevice(1))
+
+
+class LossKernels:
+    """Keeps the leading dimensions that the cross entropy was given, and refuses those that
+    the library refuses."""
+
+    def __init__(self):
+        self.lds = []
+
+    def workspace_size(self, T, V, H, train):
+        return 0
+
+    def forward(self, T, V, H, x, ld_x, w, ld_w, labels, loss, lse, ws):
+        self.lds.append((ld_x, ld_w))
+        for t, rows, ld in ((x, T, ld_x), (w, V, ld_w)):
+            assert H <= ld < 2 ** 22 and ld % 8 == 0 and t.data_ptr() % 16 == 0
+            assert rows <= 1 or ld == t.stride(0)
+        z = x.double() @ w.double().t()
+        lse.copy_(torch.logsumexp(z, 1))
+        ok = (labels >= 0) & (labels < V)
+        loss.copy_(torch.where(ok, lse - z.gather(1, labels.clamp(0, V - 1)[:, None])[:, 0], 0.0))
+
+
+@pytest.fixture
+def loss_kernels(monkeypatch):
+    k = LossKernels()
+    monkeypatch.setattr(layers.nv, "nvfp4_linear_cross_entropy", k.forward)
+    monkeypatch.setattr(layers.nv, "nvfp4_linear_cross_entropy_workspace_size", k.workspace_size)
+    monkeypatch.setattr(layers, "_on_gpu", lambda *tensors: None)
+    return k
+
+
+@pytest.mark.parametrize("batch,seq", [(1, 2 ** 16 + 8), (3, 2 ** 16 + 8), (1, 50), (3, 50)])
+def test_loss_of_the_last_tokens_of_long_sequences(loss_kernels, batch, seq):
+    """hidden[:, -1]: rows a whole sequence apart, further than the kernels' leading
+    dimension goes (2^22) for the long ones; one row has no distance at all."""
+    H = 64
+    hidden = torch.randn(1, 1, H).bfloat16().expand(batch, seq, H).contiguous()
+    hidden[:, -1] = torch.randn(batch, H).bfloat16()
+    w = torch.randn(40, H).bfloat16()
+    y = torch.arange(batch)
+    got = layers.token_cross_entropy(hidden[:, -1], w, y)
+    want = layers.token_cross_entropy(hidden[:, -1].clone(), w, y)
+    assert torch.equal(got, want) and got.shape == (batch,)
+    # a slice is read where it lies, where it can be
+    assert loss_kernels.lds[0][0] == (64 if batch == 1 or seq * H >= 2 ** 22 else seq * H)
