@@ -57,7 +57,7 @@ def _operand(t):
     other slices are copied."""
     m, ld = _rows(t)
     if ld % 8 or ld >= 2 ** 22 or m.data_ptr() % 16:
-        m, ld = m.contiguous(), m.shape[1]
+        m, ld = m.clone(memory_format=torch.contiguous_format), m.shape[1]
     return m, ld
 
 

@@ -195,3 +195,15 @@ def test_loss_of_the_last_tokens_of_long_sequences(loss_kernels, batch, seq):
     assert torch.equal(got, want) and got.shape == (batch,)
     # a slice is read where it lies, where it can be
     assert loss_kernels.lds[0][0] == (64 if batch == 1 or seq * H >= 2 ** 22 else seq * H)
+
+
+@pytest.mark.parametrize("off", [1, 4, 8])
+def test_loss_of_packed_rows_that_start_anywhere(loss_kernels, off):
+    """Rows that lie packed but not on 16 bytes (a slice of a flat buffer) are copied too."""
+    H, T, V = 64, 5, 40
+    x = torch.randn(T * H + off).bfloat16()[off:].view(T, H)
+    w = torch.randn(V * H + off).bfloat16()[off:].view(V, H)
+    y = torch.arange(T)
+    got = layers.token_cross_entropy(x, w, y)
+    want = layers.token_cross_entropy(x.clone(), w.clone(), y)
+    assert torch.equal(got, want)
