@@ -146,7 +146,7 @@ def rms_norm_mx8(x, residual, gamma, eps: float = 1e-5):
     nv.nvfp4_rms_norm(m, r, _dt(m), rows, cols, ld, ld_r, g, _dt(g), float(eps), 0.0, 0, h, cols, None, 0, codes, scales,
                       None)
     lead = x.shape[:-1]
-    return h, codes.view(*lead, cols), scales.view(*lead, -1)
+    return h, codes.view(*lead, cols), scales.view(*lead, scales.shape[1])
 
 
 class _LinearCrossEntropy(torch.autograd.Function):

@@ -272,3 +272,19 @@ def test_loss_of_the_last_tokens_of_long_sequences():
     linear_cross_entropy(packed, w, y).backward()
     assert torch.equal(hidden.grad[:, -1], packed.grad) and bool((packed.grad[:2] != 0).any())
     assert bool((hidden.grad[:, :-1] == 0).all())
+
+
+def test_empty_batches():
+    """No rows, no tokens: empty outputs of the shape, zero gradients of what they share."""
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd import layers
+    x = torch.empty(2, 0, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    gamma = torch.ones(64, device="cuda", requires_grad=True)
+    w = torch.ones(10, 64, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    h, y = layers.add_rms_norm(layers.dropout(x, 0.5, 1), x, gamma)
+    loss = layers.linear_cross_entropy(y, w, torch.empty(2, 0, dtype=torch.int64, device="cuda"))
+    (loss + h.float().sum()).backward()
+    assert float(loss) == 0 and y.shape == x.grad.shape == x.shape
+    assert bool((gamma.grad == 0).all()) and bool((w.grad == 0).all())
+    _, codes, scales = layers.rms_norm_mx8(x.detach(), None, gamma.detach())
+    assert codes.shape == (2, 0, 64) and scales.shape == (2, 0, 2)

@@ -207,3 +207,14 @@ def test_loss_of_packed_rows_that_start_anywhere(loss_kernels, off):
     got = layers.token_cross_entropy(x, w, y)
     want = layers.token_cross_entropy(x.clone(), w.clone(), y)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("lead", [(0,), (3, 0), (0, 5), (2, 3), ()])
+def test_eight_bit_norm_of_any_leading_dimensions(monkeypatch, lead):
+    """An empty batch gives empty outputs of its shape."""
+    monkeypatch.setattr(layers.nv, "nvfp4_rms_norm", lambda *a: None)
+    monkeypatch.setattr(layers, "_on_gpu", lambda *tensors: None)
+    x = torch.ones(*lead, 72).bfloat16()
+    h, codes, scales = layers.rms_norm_mx8(x, x, torch.ones(72))
+    assert h.shape == x.shape and codes.shape == (*lead, 72) and scales.shape == (*lead, 3)
+    assert codes.dtype == torch.float8_e4m3fn and scales.dtype == torch.float8_e8m0fnu
