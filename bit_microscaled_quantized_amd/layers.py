@@ -36,6 +36,8 @@ def _norm_args(x, residual, gamma):
     if x.dim() == 0 or gamma.shape != x.shape[-1:]:
         raise ValueError(f"gamma must have the shape of x's last dimension, got {tuple(gamma.shape)} for "
                          f"{tuple(x.shape)}")
+    if x.shape[-1] == 0:
+        raise ValueError("expected at least one column")
     if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
         raise ValueError("residual must have x's shape and type")
     m, ld = _rows(x)
@@ -45,8 +47,10 @@ def _norm_args(x, residual, gamma):
 
 def _rows(t):
     """t as a matrix of its last dimension with unit stride (a copy only where that
-    cannot be viewed), and its leading dimension."""
-    m = t.reshape(-1, t.shape[-1])
+    cannot be viewed), and its leading dimension.  A scalar is one element, and a tensor
+    whose rows are empty has none."""
+    cols = t.shape[-1] if t.dim() > 0 else 1
+    m = t.reshape(-1, cols) if cols > 0 else t.reshape(0, 1)
     if m.stride(1) != 1 and m.shape[1] > 1 or m.stride(0) < m.shape[1] and m.shape[0] > 1:
         m = m.contiguous()
     return m, max(m.stride(0), m.shape[1])
@@ -157,6 +161,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
         _on_gpu(x, w, labels)
         if w.dim() != 2 or x.shape[-1:] != w.shape[1:] or labels.numel() * w.shape[1] != x.numel():
             raise ValueError("expected x [..., H], weight [V, H] and one label per token")
+        if w.shape[1] == 0:
+            raise ValueError("expected at least one column")
         if labels.is_floating_point() or labels.is_complex():
             raise TypeError(f"expected integer labels, got {labels.dtype}")
         m, ld = _operand(x)

@@ -288,3 +288,14 @@ def test_empty_batches():
     assert bool((gamma.grad == 0).all()) and bool((w.grad == 0).all())
     _, codes, scales = layers.rms_norm_mx8(x.detach(), None, gamma.detach())
     assert codes.shape == (2, 0, 64) and scales.shape == (2, 0, 2)
+
+
+def test_dropout_of_scalars_and_empty_rows():
+    torch = gpuio.torch_cuda()
+    from bit_microscaled_quantized_amd.layers import dropout
+    for shape in ((), (1,), (3, 0), (0, 4)):
+        x = torch.ones(shape, device="cuda", requires_grad=True)
+        y = dropout(x, 0.25, 6)
+        y.sum().backward()
+        assert y.shape == x.grad.shape == x.shape and torch.equal(x.grad, y)
+        assert bool(((y == 0) | ((y - 4 / 3).abs() < 1e-6)).all())

@@ -218,3 +218,35 @@ def test_eight_bit_norm_of_any_leading_dimensions(monkeypatch, lead):
     h, codes, scales = layers.rms_norm_mx8(x, x, torch.ones(72))
     assert h.shape == x.shape and codes.shape == (*lead, 72) and scales.shape == (*lead, 3)
     assert codes.dtype == torch.float8_e4m3fn and scales.dtype == torch.float8_e8m0fnu
+
+
+@pytest.mark.parametrize("shape", [(), (1,), (0,), (3, 0), (0, 4), (2, 3, 4)])
+def test_dropout_of_any_shape(monkeypatch, shape):
+    """Scalars and empty tensors included, in both directions; the library sees a matrix
+    that its checks take."""
+    calls = []
+
+    def dropout(x, dt, rows, cols, ld_x, p, seed, y, ld_y):
+        assert rows >= 0 and cols >= 1 and ld_x >= cols and ld_y >= cols and x.shape == (rows, cols)
+        calls.append(rows * cols)
+        y.copy_(x.view(y.shape) * 2)
+    monkeypatch.setattr(layers.nv, "nvfp4_dropout", dropout)
+    monkeypatch.setattr(layers, "_on_gpu", lambda *tensors: None)
+    x = torch.randn(shape, requires_grad=True)
+    y = layers.dropout(x, 0.5, 3)
+    y.sum().backward()
+    assert torch.equal(y, 2 * x) and x.grad.shape == x.shape and bool((x.grad == 2).all())
+    assert calls == [x.numel()] * 2
+    with pytest.raises(TypeError):
+        layers.dropout(torch.ones(shape, dtype=torch.float16), 0.5, 3)
+
+
+def test_rows_without_columns_are_refused(monkeypatch):
+    """A norm or a product over nothing has no value."""
+    monkeypatch.setattr(layers, "_on_gpu", lambda *tensors: None)
+    x, w, y = torch.empty(3, 0).bfloat16(), torch.empty(7, 0).bfloat16(), torch.zeros(3, dtype=torch.int64)
+    for norm_of in (layers.add_rms_norm, layers.rms_norm_mx8):
+        with pytest.raises(ValueError, match="column"):
+            norm_of(x, None, torch.empty(0))
+    with pytest.raises(ValueError, match="column"):
+        layers.token_cross_entropy(x, w, y)
