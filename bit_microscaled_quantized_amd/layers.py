@@ -161,6 +161,9 @@ class _LinearCrossEntropy(torch.autograd.Function):
         _on_gpu(x, w, labels)
         if w.dim() != 2 or x.shape[-1:] != w.shape[1:] or labels.numel() * w.shape[1] != x.numel():
             raise ValueError("expected x [..., H], weight [V, H] and one label per token")
+        lead, own = ([n for n in shape if n != 1] for shape in (x.shape[:-1], labels.shape))
+        if lead != own and len(lead) > 1 and len(own) > 1:  # flat on either side, the order is plain
+            raise ValueError(f"expected one label per token, got labels {tuple(labels.shape)} for x {tuple(x.shape)}")
         if w.shape[1] == 0:
             raise ValueError("expected at least one column")
         if labels.is_floating_point() or labels.is_complex():
@@ -197,7 +200,8 @@ class _LinearCrossEntropy(torch.autograd.Function):
 
 
 def token_cross_entropy(x, w, labels):
-    """Loss of each token (0 where its label is outside [0, V)), FP32."""
+    """Loss of each token (0 where its label is outside [0, V)), FP32.  labels have x's
+    leading dimensions, or are flat in their order; the loss has the labels' shape."""
     return _LinearCrossEntropy.apply(x, w, labels)
 
 

@@ -250,3 +250,18 @@ def test_rows_without_columns_are_refused(monkeypatch):
             norm_of(x, None, torch.empty(0))
     with pytest.raises(ValueError, match="column"):
         layers.token_cross_entropy(x, w, y)
+
+
+def test_labels_belong_to_their_tokens(loss_kernels):
+    """Labels of the tokens' own shape, or flat, in their order; transposed ones, as many
+    as there are tokens, would score every token by another's label."""
+    x, w = torch.randn(2, 3, 64).bfloat16(), torch.randn(10, 64).bfloat16()
+    y = torch.arange(6).view(2, 3)
+    want = layers.token_cross_entropy(x, w, y)
+    assert want.shape == (2, 3)
+    for same in (y.view(6), y[..., None], y[None]):
+        assert torch.equal(layers.token_cross_entropy(x, w, same).view(2, 3), want)
+    assert torch.equal(layers.token_cross_entropy(x.view(6, 64), w, y), want)
+    for wrong in (y.t(), y.view(1, 3, 2), y.view(3, 2)):
+        with pytest.raises(ValueError, match="label"):
+            layers.token_cross_entropy(x, w, wrong)
