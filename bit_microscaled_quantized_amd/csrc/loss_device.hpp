@@ -16,8 +16,9 @@ typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// exp(a): one multiply and the hardware's 2^x, within 1 ulp of exp(a (1 + 2^-24));
-// results below 2^-126 are 0.
+// exp(a): one multiply and the hardware's 2^x, within 1 ulp of exp(a (1 + e)), |e| <
+// 2^-24 + 2^-26 (the product's rounding, and log2(e)'s to FP32); results below 2^-126
+// are 0.
 __device__ __forceinline__ float exp_fast(float a) { return __builtin_amdgcn_exp2f(a * kLog2e); }
 
 // (maximum m, sum of exp(z - m)) of some of a token's logits.  An infinite

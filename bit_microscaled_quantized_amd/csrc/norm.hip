@@ -563,6 +563,11 @@ __global__ __launch_bounds__(DG * 32) void k_dgamma(const float* partial, uint32
 // A backward pass keeps about two workgroups of 640 lanes on each CU of a 256-CU
 // MI355X, or one of up to 1024 for wider rows: more of them write more partial
 // sums than their overlap gains (8192 x 5120, before loads went ahead: 92 us at 512 workgroups, 115 at 1024).
+// Six waves a SIMD hold two workgroups of up to 768 lanes; rows that would take more than
+// 640 run level with one vector a lane in 768 or two in half as many (two against one: BF16
+// 8192 x 5248 84.0 us against 83.5, 8192 x 6144 97.1 / 97.3, 1000 x 6144 24.2 / 22.8;
+// FP32 4096 x 3000 53.9 / 50.5, but 1023 x 24576, where the same bound sets how many
+// workgroups there are, 194 / 215).
 constexpr int64_t kCus = 256;
 constexpr int kBackThreads = 640;
 
@@ -662,7 +667,11 @@ BackShape back_shape(int64_t rows, int64_t cols, int N) {
   BackShape b;
   const int64_t vecs = (cols + N - 1) / N;
   b.row = row_shape(vecs, vecs <= kBackThreads ? 1 : 2);
-  if (b.row.vpt * N > 32) b.row = RowShape{0, 0};  // beyond the registers
+  // Beyond the registers.  FP32 rows of eight vectors a lane are past the limit already and
+  // spill 59 of them (1023 x 20479, five vectors, 103 us; 1023 x 20484, eight, 183; 1023 x
+  // 32768 225, and 33000 columns read twice 248).  BF16 8192 x 24576 387 us, 24584 columns
+  // read twice 1090.
+  if (b.row.vpt * N > 32) b.row = RowShape{0, 0};
   if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
   // a few rows: one workgroup, whose sums are dgamma itself, ends before a second launch would
   const int all = 1024 / b.row.G;
