@@ -11,7 +11,7 @@ both directions, the norm keeps h and one number per row, the loss keeps one num
 per token and neither logits nor probabilities.  Formulas and rounding are those of
 include/nvfp4_layers.h.  BF16 and FP32 tensors (the loss BF16), any leading
 dimensions; rows may be slices of a wider buffer.  Everything runs on torch's
-current stream, with buffers from its caching allocator.
+current stream, on the current device, with buffers from its caching allocator.
 """
 from __future__ import annotations
 
