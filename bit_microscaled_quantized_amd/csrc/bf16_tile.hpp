@@ -1,4 +1,5 @@
-// One tile of a BF16 matrix product with FP32 accumulation on gfx950, 256 x 256
+// One tile of a matrix product on gfx950, BF16 with FP32 accumulation or 8-bit
+// integers with 32-bit accumulation (MfmaInt8), 256 x 256
 // (W = 4), 128 x 128 (W = 2) or 64 x 64 (W = 1, K along the rows only):
 //   acc(m, n) = sum_k A(m, k) B(n, k)
 // for operands that hold K along their rows (element (m, k) at p[m * ld + k]) or
@@ -32,6 +33,10 @@
 // k = 8 h .. 8 h + 7; of the result, column n = lr and rows 8 (r >> 2) + 4 h +
 // (r & 3), r = 0 .. 15.
 //
+// 8-bit integers take K along the rows only, two to an element of what follows: ld,
+// K and a stage's 64 count pairs, and a matrix instruction (32 x 32 x 32) reads the 16
+// bytes of a lane as 16 of them.
+//
 // Addresses stay inside the operands: rows of a tile past the last are fetched
 // from the last row (or, KMAJOR, from the last 8 columns) and never used, and a
 // KMAJOR operand's values of k past its last from that one.  K along rows may end
@@ -57,6 +62,23 @@ constexpr int TILE_THREADS = 256;
 constexpr int tile_side(int W) { return 64 * W; }
 constexpr int tile_operand(int W) { return tile_side(W) * TILE_K * 2; }  // bytes of an operand's stage
 constexpr int tile_lds(int W) { return 4 * tile_operand(W); }            // two buffers of both operands
+
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef int intx16 __attribute__((ext_vector_type(16)));
+
+// The matrix instruction of a tile: 16 bytes of either operand a lane.
+struct MfmaBf16 {
+  typedef floatx16 Acc;
+  static __device__ __forceinline__ Acc mul(bf16x8_t a, bf16x8_t b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+struct MfmaInt8 {
+  typedef intx16 Acc;
+  static __device__ __forceinline__ Acc mul(bf16x8_t a, bf16x8_t b, Acc c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(intx4, a), __builtin_bit_cast(intx4, b), c, 0, 0, 0);
+  }
+};
 
 // An operand of a tile: its first element (m = the tile's first row, k = 0),
 // leading dimension, and rows from there on (at least one; KMAJOR: rounded up to
@@ -169,9 +191,9 @@ struct TileFrag {
 // there); without it both operands have K along their rows.  All waves of the
 // workgroup take part; the caller's LDS stages are free again after its next
 // barrier.
-template <int W, bool AMAJ, bool BMAJ, bool EVEN>
+template <int W, bool AMAJ, bool BMAJ, bool EVEN, typename Op = MfmaBf16>
 __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOperand& b, int K, int kt0, int kt1,
-                                             uint8_t* lds, floatx16 (&acc)[W][W]) {
+                                             uint8_t* lds, typename Op::Acc (&acc)[W][W]) {
   constexpr int OPERAND = tile_operand(W), STAGE = 2 * OPERAND;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -191,7 +213,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
 #pragma unroll
     for (int j = 0; j < W; j++)
 #pragma unroll
-      for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < 16; r++) acc[i][j][r] = 0;
   bf16x8_t va[2][W], vb[2][W];
 
   // The stage that ends past K, and one more where the rest is odd, go first,
@@ -222,7 +244,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
         for (int i = 0; i < W; i++)
 #pragma unroll
           for (int j = 0; j < W; j++)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[0][i], vb[0][j], acc[i][j], 0, 0, 0);
+            acc[i][j] = Op::mul(va[0][i], vb[0][j], acc[i][j]);
       }
       __syncthreads();
     };
@@ -270,8 +292,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
 #define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                      \
   do {                                                                                                 \
     _Pragma("unroll") for (int m = 0; m < W * W; m++) {                                                \
-      acc[m / W][m % W] =                                                                              \
-          __builtin_amdgcn_mfma_f32_32x32x16_bf16(va[q][m / W], vb[q][m % W], acc[m / W][m % W], 0, 0, 0); \
+      acc[m / W][m % W] = Op::mul(va[q][m / W], vb[q][m % W], acc[m / W][m % W]);                       \
       TILE_FENCE;                                                                                      \
       if (m < W) {                                                                                     \
         TILE_READ(rst, rs, 1 - (q), 2 * m);                                                            \

@@ -1,0 +1,222 @@
+// The product of 8-bit integers with a scale per token and per output channel
+// (nvfp4_int8_gemm), for gfx950:
+//   c[m][n] = (sum_k a[m][k] b[n][k]) * b_scales[n] * a_scales[m]
+//
+// The sum is exact in 32 bits whatever its order, so the split of K and the order
+// of the tiles do not show in the result.  Tiles are those of bf16_tile.hpp on the
+// 8-bit matrix instruction; the weight b is a tile's first operand, whose rows a lane
+// holds four in a row of (the output's columns), so that it stores pieces of four.
+// Where the tiles are few, K is split: parts leave their integers in the workspace,
+// in the order of the lanes, and a second launch adds and scales them.
+#include "bf16_tile.hpp"
+#include "blocks_launch.hpp"
+#include "per_device.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+struct GemmArgs {
+  const int8_t* a;
+  const int8_t* b;
+  const float* a_scales;
+  const float* b_scales;
+  void* c;
+  int* partial;  // null: whole tiles
+  int64_t lda, ldb, ldc;
+  int M, N, K, parts;
+};
+
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4), may_alias));
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2), may_alias));
+
+// Four output columns from n on of row m.
+template <typename OutT>
+__device__ __forceinline__ void store_four(const GemmArgs& g, int m, int n, const intx4& v, const float* bs, float as) {
+  float f[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) f[e] = ((float)v[e] * bs[e]) * as;
+  OutT* p = static_cast<OutT*>(g.c) + (int64_t)m * g.ldc + n;
+  if (n + 4 <= g.N) {
+    if constexpr (sizeof(OutT) == 4)
+      *reinterpret_cast<f32x4_a4*>(p) = f32x4_a4{f[0], f[1], f[2], f[3]};
+    else
+      *reinterpret_cast<u32x2_a2*>(p) = u32x2_a2{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3])};
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++)
+    if (n + e < g.N) {
+      if constexpr (sizeof(OutT) == 4)
+        p[e] = f[e];
+      else
+        p[e] = (uint16_t)bf16_pack(f[e], 0.0f);
+    }
+}
+
+// Scales of four columns from n on (zeros past the last).
+__device__ __forceinline__ void four_scales(const GemmArgs& g, int n, float* bs) {
+#pragma unroll
+  for (int e = 0; e < 4; e++) bs[e] = n + e < g.N ? g.b_scales[n + e] : 0.0f;
+}
+
+template <int W, bool EVEN, typename OutT>
+__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_int8_tile(GemmArgs g) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  constexpr int TILE = tile_side(W), WAVE = 32 * W;
+  const int num_m = (g.M + TILE - 1) / TILE, num_n = (g.N + TILE - 1) / TILE, tiles = num_m * num_n;
+  const int part = blockIdx.x / tiles, t = blockIdx.x - part * tiles;
+  int pm, pn;
+  tile_place(t, num_n, num_m, pn, pm);
+  const int m0 = pm * TILE, n0 = pn * TILE;
+  const int KT = (g.K / 2 + TILE_K - 1) / TILE_K;
+  const int kt0 = (int)((int64_t)KT * part / g.parts), kt1 = (int)((int64_t)KT * (part + 1) / g.parts);
+  const TileOperand wt{reinterpret_cast<const uint16_t*>(g.b + (int64_t)n0 * g.ldb), (uint32_t)(g.ldb / 2), g.N - n0, 0};
+  const TileOperand tok{reinterpret_cast<const uint16_t*>(g.a + (int64_t)m0 * g.lda), (uint32_t)(g.lda / 2), g.M - m0, 0};
+  intx16 acc[W][W];
+  tile_product<W, false, false, EVEN, MfmaInt8>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, lr = lane & 31;
+  if (g.partial != nullptr) {
+    intx4* out = reinterpret_cast<intx4*>(g.partial) + (int64_t)blockIdx.x * (W * W * 4 * TILE_THREADS) + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < W; i++)
+#pragma unroll
+      for (int j = 0; j < W; j++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          out[((i * W + j) * 4 + q) * TILE_THREADS] =
+              intx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
+  const int nb = n0 + (wave >> 1) * WAVE + 4 * h, mb = m0 + (wave & 1) * WAVE + lr;
+  float as[W];
+#pragma unroll
+  for (int j = 0; j < W; j++) as[j] = mb + 32 * j < g.M ? g.a_scales[mb + 32 * j] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; i++) {
+    float bs[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) four_scales(g, nb + 32 * i + 8 * q, bs[q]);
+#pragma unroll
+    for (int j = 0; j < W; j++) {
+      if (mb + 32 * j >= g.M) continue;
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        store_four<OutT>(g, mb + 32 * j, nb + 32 * i + 8 * q,
+                         intx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
+                         bs[q], as[j]);
+    }
+  }
+}
+
+// The parts' sums of one of a tile's W * W * 4 planes of pieces.
+template <int W, typename OutT>
+__global__ __launch_bounds__(TILE_THREADS) void k_int8_join(GemmArgs g) {
+  constexpr int TILE = tile_side(W), WAVE = 32 * W, PLANES = W * W * 4;
+  const int num_m = (g.M + TILE - 1) / TILE, num_n = (g.N + TILE - 1) / TILE, tiles = num_m * num_n;
+  const int t = blockIdx.x / PLANES, plane = blockIdx.x % PLANES;
+  int pm, pn;
+  tile_place(t, num_n, num_m, pn, pm);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, lr = lane & 31;
+  const int i = plane / (4 * W), j = plane / 4 % W, q = plane % 4;
+  const int n = pn * TILE + (wave >> 1) * WAVE + 4 * h + 32 * i + 8 * q;
+  const int m = pm * TILE + (wave & 1) * WAVE + lr + 32 * j;
+  if (m >= g.M || n >= g.N) return;
+  const intx4* in = reinterpret_cast<const intx4*>(g.partial) + ((int64_t)t * PLANES + plane) * TILE_THREADS + threadIdx.x;
+  intx4 v{0, 0, 0, 0};
+#pragma unroll 4
+  for (int p = 0; p < g.parts; p++) v += in[(int64_t)p * tiles * PLANES * TILE_THREADS];
+  float bs[4];
+  four_scales(g, n, bs);
+  store_four<OutT>(g, m, n, v, bs, g.a_scales[m]);
+}
+
+int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
+
+// Time of a product in microseconds on 256 CUs: one large tile a CU, two or four of the
+// smaller ones, in rounds.
+double round_us(int64_t tiles, double stages, int W) {
+  const int64_t slots = W == 4 ? 256 : W == 2 ? 512 : 1024;
+  const double stage = W == 4 ? 1.55 : W == 2 ? 1.05 : 0.7, around = W == 4 ? 10.0 : 4.0;
+  return (double)((tiles + slots - 1) / slots) * (stages * stage + around);
+}
+
+struct Plan {
+  int W, parts;
+  int64_t tiles, bytes;
+};
+// split false: whole tiles only
+Plan plan_of(int64_t M, int64_t N, int64_t K, bool split) {
+  const int64_t stages = (K / 2 + TILE_K - 1) / TILE_K;
+  Plan best{4, 1, tiles_of(M, 4) * tiles_of(N, 4), 0};
+  double best_us = 1e300;
+  for (int W : {4, 2, 1}) {
+    const int64_t tiles = tiles_of(M, W) * tiles_of(N, W), slots = W == 4 ? 256 : W == 2 ? 512 : 1024;
+    if (tiles > (int64_t(1) << 22)) continue;  // the lanes of a launch fit 32 bits
+    const int64_t most = split ? std::max<int64_t>(1, std::min<int64_t>(slots / tiles, stages / 4)) : 1;
+    for (int64_t parts = 1; parts <= most; parts++) {
+      const int64_t bytes = parts == 1 ? 0 : parts * tiles * tile_side(W) * tile_side(W) * 4;
+      const double us = round_us(tiles * parts, (double)((stages + parts - 1) / parts), W) +
+                        (parts == 1 ? 0.0 : 3.0 + (double)bytes * 2.0 / 4.5e6);
+      if (us < best_us * 0.99) {
+        best_us = us;
+        best = Plan{W, (int)parts, tiles, bytes};
+      }
+    }
+  }
+  return best;
+}
+
+template <int W, bool EVEN, typename OutT>
+hipError_t allow_tile() {
+  static std::atomic<uint64_t> done{0};
+  if (tile_lds(W) <= 64 * 1024) return hipSuccess;
+  return once_per_device(done, [] {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_int8_tile<W, EVEN, OutT>),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds(W));
+  });
+}
+
+template <int W, typename OutT>
+hipError_t gemm_w(const GemmArgs& g, const Plan& p, hipStream_t s) {
+  const unsigned grid = (unsigned)(p.tiles * p.parts);
+  // a whole number of pairs of stages for every part
+  const bool even = g.K % (4 * TILE_K) == 0 && p.parts == 1;
+  hipError_t e;
+  if (even) {
+    e = allow_tile<W, true, OutT>();
+    if (e == hipSuccess) k_int8_tile<W, true, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
+  } else {
+    e = allow_tile<W, false, OutT>();
+    if (e == hipSuccess) k_int8_tile<W, false, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
+  }
+  if (e == hipSuccess) e = hipGetLastError();
+  if (e != hipSuccess || p.parts == 1) return e;
+  k_int8_join<W, OutT><<<(unsigned)(p.tiles * W * W * 4), TILE_THREADS, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+template <typename OutT>
+hipError_t gemm_t(const GemmArgs& g, const Plan& p, hipStream_t s) {
+  if (p.W == 4) return gemm_w<4, OutT>(g, p, s);
+  if (p.W == 2) return gemm_w<2, OutT>(g, p, s);
+  return gemm_w<1, OutT>(g, p, s);
+}
+
+}  // namespace
+
+int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) { return M == 0 ? 0 : plan_of(M, N, K, true).bytes; }
+
+hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* a_scales,
+                            const int8_t* b, int64_t ldb, const float* b_scales, void* c, int c_dt, int64_t ldc,
+                            void* workspace, int64_t workspace_bytes, hipStream_t s) {
+  Plan p = plan_of(M, N, K, true);
+  if (workspace == nullptr || workspace_bytes < p.bytes) p = plan_of(M, N, K, false);
+  const GemmArgs g{a,   b,   a_scales, b_scales, c,      p.parts > 1 ? static_cast<int*>(workspace) : nullptr,
+                   lda, ldb, ldc,      (int)M,   (int)N, (int)K,
+                   p.parts};
+  return c_dt == 0 ? gemm_t<uint16_t>(g, p, s) : gemm_t<float>(g, p, s);
+}
+
+}  // namespace nvfp4

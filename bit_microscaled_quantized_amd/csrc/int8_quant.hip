@@ -1,0 +1,136 @@
+// Codes and scale of each row of a tensor, or of a gated activation
+// (nvfp4_int8_quantize, nvfp4_int8_quantize_gated), for gfx950.
+//
+// Bound by HBM: a group of lanes holds a row in registers between its largest
+// magnitude and its codes, so each input is read once; rows wider than a
+// workgroup's registers are read (and the activation formed) twice.
+#include "act_device.hpp"
+#include "blocks_launch.hpp"
+#include "row_codes.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+struct QuantArgs {
+  const void* gate;
+  const void* up;
+  int8_t* codes;
+  float* scales;
+  int64_t ld_g, ld_u, ld_codes;
+  uint32_t rows, cols, padded;  // padded: cols up to a multiple of 16
+};
+
+// v of eight elements
+template <typename T, int ACT, bool STREAM>
+__device__ __forceinline__ void values_of(const QuantArgs& a, const Eight<T, STREAM>& g, const Eight<T, STREAM>& u,
+                                          float* f) {
+  g.unpack(f);
+  float fu[8];
+  if (a.up != nullptr) u.unpack(fu);
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    f[i] = act_of<ACT>(f[i]);
+    if (a.up != nullptr) f[i] *= fu[i];
+  }
+}
+
+template <typename T, int ACT, int VPT, bool STREAM>
+__global__ __launch_bounds__(1024) void k_int8_rows(QuantArgs a, int G) {
+  __shared__ uint32_t red[16];
+  const uint32_t row = blockIdx.x * (blockDim.x / G) + threadIdx.x / G, j = threadIdx.x % G;
+  const bool live = row < a.rows;
+  const T* gr = static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g;
+  const T* ur = static_cast<const T*>(a.up) + (int64_t)row * a.ld_u;
+  Eight<T, STREAM> g[VPT], u[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    const uint32_t c = (j + k * G) * 8;
+    const int n = live && c < a.cols ? (int)min(a.cols - c, 8u) : 0;
+    g[k].load(gr + c, n);
+    if (a.up != nullptr) u[k].load(ur + c, n);
+  }
+  float f[VPT][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    values_of<T, ACT, STREAM>(a, g[k], u[k], f[k]);  // zeros past the row's end
+    m = most_of<8>(f[k], m);
+  }
+  const RowCode q(group_max(m, G, red));
+  if (!live) return;
+  if (j == 0) a.scales[row] = q.scale;
+  int8_t* out = a.codes + (int64_t)row * a.ld_codes;
+#pragma unroll
+  for (int k = 0; k < VPT; k++) {
+    const uint32_t c = (j + k * G) * 8;
+    if (c < a.padded) store_codes<8>(q, f[k], out, c);
+  }
+}
+
+// Wider rows: one workgroup a row.
+template <typename T, int ACT>
+__global__ __launch_bounds__(1024) void k_int8_wide(QuantArgs a) {
+  __shared__ uint32_t red[16];
+  const uint32_t row = blockIdx.x;
+  const T* gr = static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g;
+  const T* ur = static_cast<const T*>(a.up) + (int64_t)row * a.ld_u;
+  auto at = [&](uint64_t c, float* f) {
+    const int n = c < a.cols ? (int)min((uint64_t)8, a.cols - c) : 0;
+    Eight<T, false> g, u;
+    g.load(gr + c, n);
+    if (a.up != nullptr) u.load(ur + c, n);
+    values_of<T, ACT, false>(a, g, u, f);
+  };
+  uint32_t m = 0;
+  for (uint64_t c = threadIdx.x * 8; c < a.cols; c += 1024 * 8) {
+    float f[8];
+    at(c, f);
+    m = most_of<8>(f, m);
+  }
+  const RowCode q(group_max(m, 1024, red));
+  if (threadIdx.x == 0) a.scales[row] = q.scale;
+  int8_t* out = a.codes + (int64_t)row * a.ld_codes;
+  for (uint64_t c = threadIdx.x * 8; c < a.padded; c += 1024 * 8) {
+    float f[8];
+    at(c, f);
+    *reinterpret_cast<u32x2_t*>(out + c) = u32x2_t{q.four(f), q.four(f + 4)};
+  }
+}
+
+template <typename T, int ACT>
+hipError_t quantize_t(const QuantArgs& a, hipStream_t s) {
+  const int64_t vecs = a.padded / 8;
+  const RowShape r = row_shape(vecs, a.rows >= 1024 && vecs > 128 ? 2 : 1);
+  if (r.vpt == 0 || r.vpt > 5) {
+    k_int8_wide<T, ACT><<<a.rows, 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const int threads = r.G < 64 ? 256 / r.G * r.G : r.G;
+  const unsigned grid = (a.rows + threads / r.G - 1) / (threads / r.G);
+  const bool stream = (int64_t)a.rows * a.cols * (int64_t)sizeof(T) * (a.up == nullptr ? 1 : 2) >= kStreamBytes;
+  with_vpt(r.vpt, [&](auto vpt) {
+    constexpr int VPT = vpt.value <= 5 ? vpt.value : 1;
+    if (stream)
+      k_int8_rows<T, ACT, VPT, true><<<grid, threads, 0, s>>>(a, r.G);
+    else
+      k_int8_rows<T, ACT, VPT, false><<<grid, threads, 0, s>>>(a, r.G);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_quantize(int act, const void* gate, const void* up, int dt, int64_t rows, int64_t cols,
+                                int64_t ld_g, int64_t ld_u, int8_t* codes, int64_t ld_codes, float* scales,
+                                hipStream_t s) {
+  const QuantArgs a{gate, up,       codes,          scales,         ld_g,
+                    ld_u, ld_codes, (uint32_t)rows, (uint32_t)cols, (uint32_t)((cols + 15) / 16 * 16)};
+  hipError_t e = hipSuccess;
+  with_act(act, [&](auto kind) {
+    e = dt == 0 ? quantize_t<uint16_t, kind.value>(a, s) : quantize_t<float, kind.value>(a, s);
+  });
+  return e;
+}
+
+}  // namespace nvfp4

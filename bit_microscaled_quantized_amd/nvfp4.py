@@ -18,6 +18,8 @@ NVFP4_OK, NVFP4_EINVAL, NVFP4_ESHAPE, NVFP4_EALIGN, NVFP4_EHIP, NVFP4_ESCRATCH =
 NVFP4_BF16, NVFP4_F32 = 0, 1
 NVFP4_RNE, NVFP4_SR = 0, 1
 NVFP4_ROW_1D, NVFP4_COL_1D, NVFP4_TILE_2D = 0, 1, 2
+NVFP4_ACT_NONE, NVFP4_ACT_SILU, NVFP4_ACT_GELU, NVFP4_ACT_RELU2 = range(4)
+NVFP4_GATE_LINEAR, NVFP4_GATE_SIGMOID = 0, 1
 
 EXPORTED = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_quantize_row_rht", "nvfp4_gemm",
             "nvfp4_gemm_noalloc", "nvfp4_gemm_bf16", "nvfp4_dequantize", "nvfp4_gemm_workspace_size",
@@ -25,7 +27,10 @@ EXPORTED = ("nvfp4_quantize", "nvfp4_rht_quantize", "nvfp4_quantize_row_rht", "n
             "nvfp4_status_str", "mxfp4_quantize", "mxfp4_gemm", "nvfp4_dropout", "nvfp4_rms_norm",
             "nvfp4_rms_norm_backward", "nvfp4_rms_norm_backward_workspace_size",
             "nvfp4_linear_cross_entropy", "nvfp4_linear_cross_entropy_backward",
-            "nvfp4_linear_cross_entropy_workspace_size")
+            "nvfp4_linear_cross_entropy_workspace_size", "nvfp4_int8_quantize", "nvfp4_int8_quantize_gated",
+            "nvfp4_int8_gemm", "nvfp4_int8_gemm_workspace_size", "nvfp4_block_norms",
+            "nvfp4_block_norms_backward", "nvfp4_block_norms_backward_workspace_size", "nvfp4_gated_act",
+            "nvfp4_gated_act_backward")
 
 _lib = None
 
@@ -101,6 +106,28 @@ def load_library():
     L.nvfp4_linear_cross_entropy_backward.restype = i32
     L.nvfp4_linear_cross_entropy_workspace_size.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i64)]
     L.nvfp4_linear_cross_entropy_workspace_size.restype = i32
+    L.nvfp4_int8_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp]
+    L.nvfp4_int8_quantize.restype = i32
+    L.nvfp4_int8_quantize_gated.argtypes = [i32, vp, vp, i32, i64, i64, i64, i64, vp, i64, vp, vp]
+    L.nvfp4_int8_quantize_gated.restype = i32
+    L.nvfp4_int8_gemm.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i32, i64, vp, i64, vp]
+    L.nvfp4_int8_gemm.restype = i32
+    L.nvfp4_int8_gemm_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.nvfp4_int8_gemm_workspace_size.restype = i32
+    L.nvfp4_block_norms.argtypes = [vp, vp, vp, i32, i64, i64, i64, i64, i64, i32, vp, vp, i32, f32, f32,
+                                    vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.nvfp4_block_norms.restype = i32
+    L.nvfp4_block_norms_backward.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, i64, i64, i64, i32,
+                                             vp, vp, i32, vp, vp, f32, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                             i64, vp]
+    L.nvfp4_block_norms_backward.restype = i32
+    L.nvfp4_block_norms_backward_workspace_size.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    L.nvfp4_block_norms_backward_workspace_size.restype = i32
+    L.nvfp4_gated_act.argtypes = [i32, vp, vp, i32, i64, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.nvfp4_gated_act.restype = i32
+    L.nvfp4_gated_act_backward.argtypes = [i32, vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i64, vp, i64, vp,
+                                           i64, vp]
+    L.nvfp4_gated_act_backward.restype = i32
     L.nvfp4_status_str.argtypes = [i32]
     L.nvfp4_status_str.restype = ctypes.c_char_p
     _lib = L
@@ -351,3 +378,82 @@ def nvfp4_linear_cross_entropy_backward(T, V, H, x, ld_x, w, ld_w, labels, lse, 
         ld_dx, _addr(dw), dw_dt, ld_dw, float(beta), _addr(workspace),
         _bytes(workspace, workspace_bytes), _stream(stream))
     return _check("nvfp4_linear_cross_entropy_backward", st, raise_on_error)
+
+
+def nvfp4_int8_quantize(x, dt, rows, cols, ld_x, codes, ld_codes, scales, stream=None,
+                        raise_on_error=True) -> int:
+    st = load_library().nvfp4_int8_quantize(_addr(x), dt, rows, cols, ld_x, _addr(codes), ld_codes,
+                                            _addr(scales), _stream(stream))
+    return _check("nvfp4_int8_quantize", st, raise_on_error)
+
+
+def nvfp4_int8_quantize_gated(act, gate, up, dt, rows, cols, ld_gate, ld_up, codes, ld_codes, scales,
+                              stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_int8_quantize_gated(act, _addr(gate), _addr(up), dt, rows, cols, ld_gate,
+                                                  ld_up, _addr(codes), ld_codes, _addr(scales),
+                                                  _stream(stream))
+    return _check("nvfp4_int8_quantize_gated", st, raise_on_error)
+
+
+def nvfp4_int8_gemm_workspace_size(M, N, K) -> int:
+    """Workspace bytes nvfp4_int8_gemm uses for this shape."""
+    out = ctypes.c_int64(0)
+    _check("nvfp4_int8_gemm_workspace_size",
+           load_library().nvfp4_int8_gemm_workspace_size(M, N, K, ctypes.byref(out)), True)
+    return out.value
+
+
+def nvfp4_int8_gemm(M, N, K, a, lda, a_scales, b, ldb, b_scales, c, c_dt, ldc, workspace=None,
+                    workspace_bytes=None, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_int8_gemm(
+        M, N, K, _addr(a), lda, _addr(a_scales), _addr(b), ldb, _addr(b_scales), _addr(c), c_dt, ldc,
+        _addr(workspace), _bytes(workspace, workspace_bytes), _stream(stream))
+    return _check("nvfp4_int8_gemm", st, raise_on_error)
+
+
+def nvfp4_block_norms(x, residual, gate, dt, rows, cols, ld_x, ld_r, ld_gate, gate_act, post_gamma,
+                      pre_gamma, gamma_dt, eps, scale, h, ld_h, y, ld_y, codes, ld_codes, scales,
+                      post_rstd, pre_rstd, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_block_norms(
+        _addr(x), _addr(residual), _addr(gate), dt, rows, cols, ld_x, ld_r, ld_gate, gate_act,
+        _addr(post_gamma), _addr(pre_gamma), gamma_dt, float(eps), float(scale), _addr(h), ld_h, _addr(y),
+        ld_y, _addr(codes), ld_codes, _addr(scales), _addr(post_rstd), _addr(pre_rstd), _stream(stream))
+    return _check("nvfp4_block_norms", st, raise_on_error)
+
+
+def nvfp4_block_norms_backward_workspace_size(rows, cols) -> int:
+    """Workspace bytes of nvfp4_block_norms_backward with sums over the rows."""
+    out = ctypes.c_int64(0)
+    _check("nvfp4_block_norms_backward_workspace_size",
+           load_library().nvfp4_block_norms_backward_workspace_size(rows, cols, ctypes.byref(out)), True)
+    return out.value
+
+
+def nvfp4_block_norms_backward(dy, dh, h, x, gate, dt, rows, cols, ld_dy, ld_dh, ld_h, ld_x, ld_gate,
+                               gate_act, post_gamma, pre_gamma, gamma_dt, post_rstd, pre_rstd, scale, dx,
+                               ld_dx, dresidual, ld_dr, dgate, ld_dgate, dpost_gamma, dpre_gamma,
+                               workspace=None, workspace_bytes=None, stream=None,
+                               raise_on_error=True) -> int:
+    st = load_library().nvfp4_block_norms_backward(
+        _addr(dy), _addr(dh), _addr(h), _addr(x), _addr(gate), dt, rows, cols, ld_dy, ld_dh, ld_h, ld_x,
+        ld_gate, gate_act, _addr(post_gamma), _addr(pre_gamma), gamma_dt, _addr(post_rstd),
+        _addr(pre_rstd), float(scale), _addr(dx), ld_dx, _addr(dresidual), ld_dr, _addr(dgate), ld_dgate,
+        _addr(dpost_gamma), _addr(dpre_gamma), _addr(workspace), _bytes(workspace, workspace_bytes),
+        _stream(stream))
+    return _check("nvfp4_block_norms_backward", st, raise_on_error)
+
+
+def nvfp4_gated_act(act, gate, up, dt, rows, cols, ld_gate, ld_up, y, ld_y, gate_codes, gate_scales,
+                    up_codes, up_scales, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_gated_act(
+        act, _addr(gate), _addr(up), dt, rows, cols, ld_gate, ld_up, _addr(y), ld_y, _addr(gate_codes),
+        _addr(gate_scales), _addr(up_codes), _addr(up_scales), _stream(stream))
+    return _check("nvfp4_gated_act", st, raise_on_error)
+
+
+def nvfp4_gated_act_backward(act, gate_codes, gate_scales, up_codes, up_scales, dy, dt, rows, cols, ld_dy,
+                             dgate, ld_dgate, dup, ld_dup, y, ld_y, stream=None, raise_on_error=True) -> int:
+    st = load_library().nvfp4_gated_act_backward(
+        act, _addr(gate_codes), _addr(gate_scales), _addr(up_codes), _addr(up_scales), _addr(dy), dt,
+        rows, cols, ld_dy, _addr(dgate), ld_dgate, _addr(dup), ld_dup, _addr(y), ld_y, _stream(stream))
+    return _check("nvfp4_gated_act_backward", st, raise_on_error)
