@@ -46,6 +46,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "int8_device.hpp"
 #include "loss_device.hpp"
 
 namespace nvfp4 {
@@ -62,9 +63,6 @@ constexpr int TILE_THREADS = 256;
 constexpr int tile_side(int W) { return 64 * W; }
 constexpr int tile_operand(int W) { return tile_side(W) * TILE_K * 2; }  // bytes of an operand's stage
 constexpr int tile_lds(int W) { return 4 * tile_operand(W); }            // two buffers of both operands
-
-typedef int intx4 __attribute__((ext_vector_type(4)));
-typedef int intx16 __attribute__((ext_vector_type(16)));
 
 // The matrix instruction of a tile: 16 bytes of either operand a lane.
 struct MfmaBf16 {

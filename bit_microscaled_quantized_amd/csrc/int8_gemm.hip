@@ -10,55 +10,12 @@
 // in the order of the lanes, and a second launch adds and scales them.
 #include "bf16_tile.hpp"
 #include "blocks_launch.hpp"
+#include "int8_device.hpp"
 #include "per_device.hpp"
 
 namespace nvfp4 {
 
 namespace {
-
-struct GemmArgs {
-  const int8_t* a;
-  const int8_t* b;
-  const float* a_scales;
-  const float* b_scales;
-  void* c;
-  int* partial;  // null: whole tiles
-  int64_t lda, ldb, ldc;
-  int M, N, K, parts;
-};
-
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4), may_alias));
-typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2), may_alias));
-
-// Four output columns from n on of row m.
-template <typename OutT>
-__device__ __forceinline__ void store_four(const GemmArgs& g, int m, int n, const intx4& v, const float* bs, float as) {
-  float f[4];
-#pragma unroll
-  for (int e = 0; e < 4; e++) f[e] = ((float)v[e] * bs[e]) * as;
-  OutT* p = static_cast<OutT*>(g.c) + (int64_t)m * g.ldc + n;
-  if (n + 4 <= g.N) {
-    if constexpr (sizeof(OutT) == 4)
-      *reinterpret_cast<f32x4_a4*>(p) = f32x4_a4{f[0], f[1], f[2], f[3]};
-    else
-      *reinterpret_cast<u32x2_a2*>(p) = u32x2_a2{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3])};
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; e++)
-    if (n + e < g.N) {
-      if constexpr (sizeof(OutT) == 4)
-        p[e] = f[e];
-      else
-        p[e] = (uint16_t)bf16_pack(f[e], 0.0f);
-    }
-}
-
-// Scales of four columns from n on (zeros past the last).
-__device__ __forceinline__ void four_scales(const GemmArgs& g, int n, float* bs) {
-#pragma unroll
-  for (int e = 0; e < 4; e++) bs[e] = n + e < g.N ? g.b_scales[n + e] : 0.0f;
-}
 
 template <int W, bool EVEN, typename OutT>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_int8_tile(GemmArgs g) {
@@ -131,6 +88,9 @@ __global__ __launch_bounds__(TILE_THREADS) void k_int8_join(GemmArgs g) {
   four_scales(g, n, bs);
   store_four<OutT>(g, m, n, v, bs, g.a_scales[m]);
 }
+
+// Up to here the weight streams past the tokens.
+constexpr int64_t kFewTokens = 64;
 
 int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
 
@@ -206,11 +166,21 @@ hipError_t gemm_t(const GemmArgs& g, const Plan& p, hipStream_t s) {
 
 }  // namespace
 
-int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) { return M == 0 ? 0 : plan_of(M, N, K, true).bytes; }
+int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
+  return M == 0 ? 0 : M <= kFewTokens ? few_plan(M, N, K).bytes : plan_of(M, N, K, true).bytes;
+}
 
 hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* a_scales,
                             const int8_t* b, int64_t ldb, const float* b_scales, void* c, int c_dt, int64_t ldc,
                             void* workspace, int64_t workspace_bytes, hipStream_t s) {
+  if (M <= kFewTokens) {
+    const FewPlan f = few_plan(M, N, K);
+    const bool split = f.parts > 1 && workspace != nullptr && workspace_bytes >= f.bytes;
+    const GemmArgs g{a,   b,   a_scales, b_scales, c,      split ? static_cast<int*>(workspace) : nullptr,
+                     lda, ldb, ldc,      (int)M,   (int)N, (int)K,
+                     split ? f.parts : 1};
+    return int8_few(g, c_dt, s);
+  }
   Plan p = plan_of(M, N, K, true);
   if (workspace == nullptr || workspace_bytes < p.bytes) p = plan_of(M, N, K, false);
   const GemmArgs g{a,   b,   a_scales, b_scales, c,      p.parts > 1 ? static_cast<int*>(workspace) : nullptr,
