@@ -46,23 +46,46 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_i
               intx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     return;
   }
-  const int nb = n0 + (wave >> 1) * WAVE + 4 * h, mb = m0 + (wave & 1) * WAVE + lr;
+  // The output leaves in whole rows of the wave's tile, through its share of the stages:
+  // RB bytes of a token at a time, the 16-byte chunk c of token m in slot c ^ (m / (256 /
+  // RB)), which is free of bank conflicts both ways.  (Stored as the lanes hold it, 16 bytes of
+  // 32 tokens at a time, a tile's end took 8 us more.)
+  constexpr int SIZE = sizeof(OutT), RB = WAVE * SIZE < 256 ? WAVE * SIZE : 256, CH = RB / 16;
+  constexpr int PASSES = WAVE * SIZE / RB, IW = W / PASSES;
+  __syncthreads();  // the stages are free
+  uint8_t* own = lds + wave * (WAVE * RB);
+  const int nb = n0 + (wave >> 1) * WAVE, mb = m0 + (wave & 1) * WAVE;
   float as[W];
 #pragma unroll
-  for (int j = 0; j < W; j++) as[j] = mb + 32 * j < g.M ? g.a_scales[mb + 32 * j] : 0.0f;
+  for (int j = 0; j < W; j++) as[j] = mb + lr + 32 * j < g.M ? g.a_scales[mb + lr + 32 * j] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < W; i++) {
-    float bs[4][4];
+  for (int p = 0; p < PASSES; p++) {
 #pragma unroll
-    for (int q = 0; q < 4; q++) four_scales(g, nb + 32 * i + 8 * q, bs[q]);
+    for (int i = 0; i < IW; i++)
 #pragma unroll
-    for (int j = 0; j < W; j++) {
-      if (mb + 32 * j >= g.M) continue;
+      for (int q = 0; q < 4; q++) {
+        float bs[4];
+        four_scales(g, nb + 32 * (p * IW + i) + 8 * q + 4 * h, bs);
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        store_four<OutT>(g, mb + 32 * j, nb + 32 * i + 8 * q,
-                         intx4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
-                         bs[q], as[j]);
+        for (int j = 0; j < W; j++) {
+          const int m = 32 * j + lr, at = (32 * i + 8 * q + 4 * h) * SIZE;
+          uint8_t* to = own + m * RB + (((at >> 4) ^ ((m / (256 / RB)) & (CH - 1))) << 4) + (at & 15);
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; e++) f[e] = ((float)acc[p * IW + i][j][4 * q + e] * bs[e]) * as[j];
+          if constexpr (SIZE == 4)
+            *reinterpret_cast<u32x4_t*>(to) = VecOf<float>::pack(f);
+          else
+            *reinterpret_cast<u32x2_t*>(to) = u32x2_t{bf16_pack(f[0], f[1]), bf16_pack(f[2], f[3])};
+        }
+      }
+#pragma unroll 8
+    for (int r = 0; r < WAVE; r += 64 / CH) {
+      const int m = r + lane / CH, c = lane % CH;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + m * RB + ((c ^ ((m / (256 / RB)) & (CH - 1))) << 4));
+      const int n = nb + (p * RB + c * 16) / SIZE;
+      if (mb + m < g.M && n < g.N)
+        store_vec<OutT>(static_cast<OutT*>(g.c) + (int64_t)(mb + m) * g.ldc + n, v, g.N - n);
     }
   }
 }
