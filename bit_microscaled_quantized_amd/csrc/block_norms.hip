@@ -42,6 +42,18 @@ __device__ __forceinline__ int inside(uint64_t c, uint32_t cols) {
   return c < cols ? (int)min((uint64_t)N, cols - c) : 0;
 }
 
+// A place in a row, `off` bytes from its start (rows in registers are narrower than 2^17
+// columns): where the row is the same all over a wave, a lane then needs no 64-bit
+// address for each tensor.
+template <typename T, typename P>
+__device__ __forceinline__ T* at_row(P* p, uint32_t row, int64_t ld, uint32_t off) {
+  T* start = static_cast<T*>(p) + (int64_t)row * ld;
+  if constexpr (std::is_const_v<T>)
+    return reinterpret_cast<T*>(reinterpret_cast<const uint8_t*>(start) + off);
+  else
+    return reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(start) + off);
+}
+
 template <typename T, bool STREAM>
 __device__ __forceinline__ u32x4_t load_or_zero(const T* p, int n) {
   return n > 0 ? load_vec<T, STREAM>(p, n) : u32x4_t{0, 0, 0, 0};
@@ -212,6 +224,11 @@ __global__ __launch_bounds__(1024) void k_block_norms_wide(NormsArgs a) {
 
 // ---- backward
 
+// Element c of a vector of BF16 or FP32.
+__device__ __forceinline__ float one_of(const void* p, int f32, uint32_t c) {
+  return f32 ? static_cast<const float*>(p)[c] : VecOf<uint16_t>::one(static_cast<const uint16_t*>(p) + c);
+}
+
 struct NormsBackArgs {
   const void* dy;
   const void* dh;
@@ -224,176 +241,311 @@ struct NormsBackArgs {
   const float* pre_rstd;
   void* dx;
   void* dr;
-  void* dgate;         // per row; null where the gate is one row for all
+  void* dgate;  // per row; null where the gate is one row for all
   float* pre_part;     // [gridDim.x][cols] sums of dy * n, or null
   float* post_part;    // the same of d * m (without the gate, where it is one row for all), or null
   int64_t ld_dy, ld_dh, ld_h, ld_x, ld_gate, ld_dx, ld_dr, ld_dgate;
   uint32_t rows, cols;
-  int gamma_f32, sigmoid, shared;  // shared: one row of gates for all
+  int gamma_f32, sigmoid;
   float scale;
 };
 
-// A lane's vector of a row, in its way through the backward pass.
-template <typename T>
-struct BackVec {
-  static constexpr int N = VecOf<T>::N;
-  // t: in, dh; out, dh + rstd * (dy * gamma - n * mean)
-  static __device__ __forceinline__ void inner(float* t, const float* dy, const float* h, const float* gamma, float rstd,
-                                               float mean) {
+// t: in, dh; out, dh + rstd * (dy * gamma - n * mean), n = h * rstd
+template <int N>
+__device__ __forceinline__ void back_vec(float* t, const float* dy, const float* h, const float* gamma, float rstd,
+                                         float mean) {
+  const float f = -(rstd * mean);
 #pragma unroll
-    for (int i = 0; i < N; i++)
-      t[i] = __builtin_fmaf(rstd, __builtin_fmaf(-(h[i] * rstd), mean, dy[i] * gamma[i]), t[i]);
-  }
-};
+  for (int i = 0; i < N; i++) t[i] = __builtin_fmaf(rstd, __builtin_fmaf(h[i], f, dy[i] * gamma[i]), t[i]);
+}
 
-// What the second half takes of t: d (the gradient of o), its sum's term and dgate.
+// A gate: none, one row for all rows, or one for each, itself or its logistic function.
+enum GateKind { kNoGate, kChannel, kToken, kTokenSigmoid };
+
+// What the second half takes of t, for N elements: b = d * gamma, d its gradient of o,
+// dgate, and d * m added to sum (without the gate of a channel).  gate: the factor of a
+// channel, a token's tensor otherwise.
 //   d = scale * t * g;  dgate = scale * t * (m * gamma) * g'
-template <typename T>
-__device__ __forceinline__ void gate_vec(const NormsBackArgs& a, const float* t, const float* m, u32x4_t gate,
-                                         const float* gamma, float* d, float* term, float* dgate) {
-  constexpr int N = VecOf<T>::N;
-  float fg[N];
-  if (a.gate != nullptr) VecOf<T>::unpack(gate, fg);
+template <int KIND, int N>
+__device__ __forceinline__ void gate_vec(float scale, const float* t, const float* m, const float* gate,
+                                         const float* gamma, float* b, float* sum, float* dgate) {
 #pragma unroll
   for (int i = 0; i < N; i++) {
-    d[i] = a.scale * t[i];
-    term[i] = d[i] * m[i];
-    if (a.gate != nullptr) {
-      const float g = a.sigmoid ? sigmoid(fg[i]) : fg[i];
-      dgate[i] = (term[i] * gamma[i]) * (a.sigmoid ? g * (1.0f - g) : 1.0f);
-      if (!a.shared) term[i] *= g;
-      d[i] *= g;
+    const float d = scale * t[i];
+    if constexpr (KIND == kToken || KIND == kTokenSigmoid) {
+      const float g = KIND == kTokenSigmoid ? sigmoid(gate[i]) : gate[i];
+      const float term = d * m[i];
+      dgate[i] = term * gamma[i];
+      if constexpr (KIND == kTokenSigmoid) dgate[i] *= __builtin_fmaf(-g, g, g);
+      sum[i] = __builtin_fmaf(term, g, sum[i]);
+      b[i] = (d * g) * gamma[i];
+    } else {
+      sum[i] = __builtin_fmaf(d, m[i], sum[i]);
+      b[i] = (KIND == kChannel ? d * gate[i] : d) * gamma[i];
     }
   }
 }
 
-template <typename T, int VPT, bool STREAM>
+// group_sum with a place in LDS of its own, which every wave has left before the
+// workgroup's last barrier but one: one barrier a sum.
+__device__ __forceinline__ float group_sum_once(float v, int G, float* red) {
+  v = span_sum(v, G);
+  if (G > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const int waves = G / 64, first = (int)threadIdx.x / G * waves, w = threadIdx.x & 15;
+    v = span_sum(w >= first && w < first + waves ? red[w] : 0.0f, 16);
+  }
+  return v;
+}
+
+// A lane's vectors of a row.
+template <int VPT>
+struct NormsRow {
+  u32x4_t dy[VPT], h[VPT], dh[VPT], x[VPT], gate[VPT];
+  float pre, post;
+};
+
+// Four values of a vector in LDS
+__device__ __forceinline__ void lds_four(const float* p, float* f) {
+  VecOf<float>::unpack(*reinterpret_cast<const u32x4_t*>(p), f);
+}
+// Elements 4 u .. 4 u + 3 of a vector, and their place in one
+template <typename T>
+__device__ __forceinline__ void unpack_four(const u32x4_t& v, int u, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    VecOf<float>::unpack(v, f);
+  } else {
+    f[0] = bf16lo(v[2 * u]), f[1] = bf16hi(v[2 * u]), f[2] = bf16lo(v[2 * u + 1]), f[3] = bf16hi(v[2 * u + 1]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void pack_four(u32x4_t& v, int u, const float* f) {
+  if constexpr (sizeof(T) == 4) {
+    v = VecOf<float>::pack(f);
+  } else {
+    v[2 * u] = bf16_pack(f[0], f[1]);
+    v[2 * u + 1] = bf16_pack(f[2], f[3]);
+  }
+}
+
+// A vector's elements from the sh-th on, zeros behind them.
+template <typename T>
+__device__ __forceinline__ void shift_down(u32x4_t& v, int sh) {
+  const int words = sizeof(T) == 4 ? sh : sh >> 1;
+  if (words & 4) v = u32x4_t{0, 0, 0, 0};
+  if (words & 2) v = u32x4_t{v[2], v[3], 0, 0};
+  if (words & 1) v = u32x4_t{v[1], v[2], v[3], 0};
+  if (sizeof(T) == 2 && (sh & 1))
+    v = u32x4_t{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+}
+
+// Another offset for all that the compiler knows: sums of it with the bases of the
+// tensors are not kept over the rows.
+__device__ __forceinline__ void opaque(uint32_t& off) { asm volatile("" : "+v"(off)); }
+
+// What a vector holds is unknown from here on: the compiler unpacks it again where it is
+// used again, rather than keep its elements (twice the registers) over a sum.
+__device__ __forceinline__ void packed(u32x4_t& v) { asm volatile("" : "+v"(v)); }
+// These sums are needed here: the compiler does not put their additions off to the end
+// of the row (and keep both factors until then).
+template <int N>
+__device__ __forceinline__ void added(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i++) asm volatile("" : "+v"(v[i]));
+}
+
+// Rows of up to G * VPT vectors: each group of G lanes walks rows with a stride, its
+// column sums in registers; the groups of a workgroup add theirs in LDS in order.
+//
+// Loads and stores complete in one order, so loads that follow a row's stores wait for
+// them as well.  So the gains (and a gate that is one row for all) lie in LDS, in FP32,
+// and where the registers hold two rows' vectors (AHEAD) the next row's loads are in
+// flight while a row is summed.
+//
+// WAVES: a group is whole waves, so its row is the same all over a wave.
+template <typename T, int VPT, int KIND, bool STREAM, bool WAVES>
 __global__ __launch_bounds__(1024, 4) void k_block_norms_back(NormsBackArgs a, int G) {
   constexpr int N = VecOf<T>::N;
-  __shared__ float red[16];
-  extern __shared__ float comb[];
+  constexpr bool AHEAD = VPT * N <= 8, TOKEN = KIND == kToken || KIND == kTokenSigmoid;
+  __shared__ float red[2][16];
+  extern __shared__ __align__(16) float gains[];
   const int groups = blockDim.x / G;
-  const int grp = threadIdx.x / G, j = threadIdx.x % G;
+  const int at = threadIdx.x / G, grp = WAVES ? __builtin_amdgcn_readfirstlane(at) : at, j = threadIdx.x % G;
+  const uint32_t width = (uint32_t)(G * VPT) * N;  // columns of the vectors in LDS, zeros past cols
   float acc_pre[VPT][N], acc_post[VPT][N];
+  // A row's last vector may end past it: it is read as the last whole one and shifted (so
+  // are the vectors behind it, by a whole one).
+  uint32_t from[VPT], to[VPT];  // bytes
+  int sh[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; k++)
+  for (int k = 0; k < VPT; k++) {
 #pragma unroll
     for (int i = 0; i < N; i++) acc_pre[k][i] = acc_post[k][i] = 0.0f;
-  for (uint32_t r0 = blockIdx.x * groups; r0 < a.rows; r0 += gridDim.x * groups) {
-    const uint32_t row = r0 + grp;
-    const bool live = row < a.rows;
-    const float pre = live ? a.pre_rstd[row] : 0.0f, post = live ? a.post_rstd[row] : 0.0f;
-    u32x4_t vdy[VPT], vh[VPT], vdh[VPT], vx[VPT], vg[VPT];
+    const uint32_t c = (j + k * G) * N;
+    from[k] = min(c, a.cols - N);
+    sh[k] = (int)min(c - from[k], (uint32_t)N);
+    from[k] *= (uint32_t)sizeof(T);
+    to[k] = c * (uint32_t)sizeof(T);
+  }
+  // without a dh, dy is read in its place and cleared
+  const void* dh = a.dh == nullptr ? a.dy : a.dh;
+  const int64_t ld_dh = a.dh == nullptr ? a.ld_dy : a.ld_dh;
+  const uint32_t dh_mask = a.dh == nullptr ? 0u : ~0u;
+  // Rows past the last are read from it (whatever follows, as many loads are in flight, which
+  // is what the waits for the row before them count) and cleared below.
+  auto load = [&](uint32_t r0, NormsRow<VPT>& v) {
+    const uint32_t row = min(r0 + grp, a.rows - 1);
+    v.pre = a.pre_rstd[row];
+    v.post = a.post_rstd[row];
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
-      const uint32_t c = (j + k * G) * N;
-      const int n = live ? inside<N>(c, a.cols) : 0;
-      vdy[k] = load_or_zero<T, STREAM>(static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy + c, n);
-      vh[k] = load_or_zero<T, STREAM>(static_cast<const T*>(a.h) + (int64_t)row * a.ld_h + c, n);
-      vdh[k] = load_or_zero<T, STREAM>(static_cast<const T*>(a.dh) + (int64_t)row * a.ld_dh + c,
-                                       a.dh == nullptr ? 0 : n);
-      vx[k] = load_or_zero<T, STREAM>(static_cast<const T*>(a.x) + (int64_t)row * a.ld_x + c, n);
-      vg[k] = load_or_zero<T, false>(static_cast<const T*>(a.gate) + (int64_t)row * a.ld_gate + c,
-                                     a.gate == nullptr ? 0 : n);
+      opaque(from[k]);
+      v.dy[k] = load_vec<T, STREAM>(at_row<const T>(a.dy, row, a.ld_dy, from[k]), N);
+      v.h[k] = load_vec<T, STREAM>(at_row<const T>(a.h, row, a.ld_h, from[k]), N);
+      v.dh[k] = load_vec<T, STREAM>(at_row<const T>(dh, row, ld_dh, from[k]), N);
+      v.x[k] = load_vec<T, STREAM>(at_row<const T>(a.x, row, a.ld_x, from[k]), N);
+      if constexpr (TOKEN) v.gate[k] = load_vec<T, STREAM>(at_row<const T>(a.gate, row, a.ld_gate, from[k]), N);
     }
+  };
+  const uint32_t step = gridDim.x * groups;
+  const float per_col = 1.0f / (float)a.cols;
+  NormsRow<VPT> next;
+  if constexpr (AHEAD) load(blockIdx.x * groups, next);
+  for (uint32_t c = threadIdx.x; c < width; c += blockDim.x) {
+    const bool in = c < a.cols;
+    gains[c] = in ? one_of(a.pre, a.gamma_f32, c) : 0.0f;
+    gains[width + c] = in ? one_of(a.post, a.gamma_f32, c) : 0.0f;
+    if constexpr (KIND == kChannel) {
+      const float g = in ? one_of(a.gate, sizeof(T) == 4, c) : 0.0f;
+      gains[2 * width + c] = a.sigmoid ? sigmoid(g) : g;
+    }
+  }
+  __syncthreads();
+  for (uint32_t r0 = blockIdx.x * groups; r0 < a.rows; r0 += step) {
+    const uint32_t row = r0 + grp;
+    NormsRow<VPT> v;
+    if constexpr (AHEAD) {
+      v = next;
+      load(r0 + step, next);  // at most 2^28 rows, and 2^20 to a step
+    } else {
+      load(r0, v);
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; k++)
+      if (sh[k] != 0 || row >= a.rows) {
+        const int by = row < a.rows ? sh[k] : N;
+        shift_down<T>(v.dy[k], by);
+        shift_down<T>(v.h[k], by);
+        shift_down<T>(v.dh[k], by);
+        shift_down<T>(v.x[k], by);
+        if constexpr (TOKEN) shift_down<T>(v.gate[k], by);
+      }
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
-      const uint32_t c = (j + k * G) * N;
-      const int n = live ? inside<N>(c, a.cols) : 0;
-      if (n <= 0) continue;
-      float dy[N], nh[N], gm[N];
-      VecOf<T>::unpack(vdy[k], dy);
-      VecOf<T>::unpack(vh[k], nh);
-      load_gamma<N>(a.pre, a.gamma_f32, c, n, gm);
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        nh[i] *= pre;
-        s = __builtin_fmaf(dy[i] * gm[i], nh[i], s);
-        acc_pre[k][i] = __builtin_fmaf(dy[i], nh[i], acc_pre[k][i]);
+      for (int u = 0; u < N / 4; u++) {
+        float dy[4], nh[4], gm[4];
+        unpack_four<T>(v.dy[k], u, dy);
+        unpack_four<T>(v.h[k], u, nh);
+        lds_four(gains + (j + k * G) * N + 4 * u, gm);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          nh[i] *= v.pre;
+          s = __builtin_fmaf(dy[i] * gm[i], nh[i], s);
+          acc_pre[k][4 * u + i] = __builtin_fmaf(dy[i], nh[i], acc_pre[k][4 * u + i]);
+        }
       }
+      packed(v.dy[k]);
+      packed(v.h[k]);
+      added(acc_pre[k]);
     }
-    const float mean_pre = group_sum(s, G, red) / (float)a.cols;
-    float d[VPT][N];
+    const float mean_pre = group_sum_once(s, G, red[0]) * per_col;
+    float b[VPT][N];
     s = 0.0f;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
       const uint32_t c = (j + k * G) * N;
-      const int n = live ? inside<N>(c, a.cols) : 0;
-      if (n <= 0) continue;
-      float dy[N], h[N], gm[N], t[N], m[N], term[N], dg[N];
-      VecOf<T>::unpack(vdy[k], dy);
-      VecOf<T>::unpack(vh[k], h);
-      VecOf<T>::unpack(vdh[k], t);  // zeros without one
-      load_gamma<N>(a.pre, a.gamma_f32, c, n, gm);
-      BackVec<T>::inner(t, dy, h, gm, pre, mean_pre);
-      if (a.dr != nullptr)
-        store_vec<T, STREAM>(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(t), n);
-      VecOf<T>::unpack(vx[k], m);
-      load_gamma<N>(a.post, a.gamma_f32, c, n, gm);
+      const int n = row < a.rows ? N - sh[k] : 0;
+      u32x4_t out_r, out_g;
+      opaque(to[k]);
 #pragma unroll
-      for (int i = 0; i < N; i++) m[i] *= post;
-      gate_vec<T>(a, t, m, vg[k], gm, d[k], term, dg);
-      if (a.dgate != nullptr)
-        store_vec<T, STREAM>(static_cast<T*>(a.dgate) + (int64_t)row * a.ld_dgate + c, VecOf<T>::pack(dg), n);
+      for (int u = 0; u < N / 4; u++) {
+        float dy[4], h[4], gm[4], t[4], m[4], gate[4], dg[4];
+        const u32x4_t vdh = v.dh[k] & dh_mask;
+        unpack_four<T>(v.dy[k], u, dy);
+        unpack_four<T>(v.h[k], u, h);
+        unpack_four<T>(vdh, u, t);
+        lds_four(gains + c + 4 * u, gm);
+        back_vec<4>(t, dy, h, gm, v.pre, mean_pre);
+        pack_four<T>(out_r, u, t);
+        unpack_four<T>(v.x[k], u, m);
+        lds_four(gains + width + c + 4 * u, gm);
+        if constexpr (TOKEN) unpack_four<T>(v.gate[k], u, gate);
+        if constexpr (KIND == kChannel) lds_four(gains + 2 * width + c + 4 * u, gate);
 #pragma unroll
-      for (int i = 0; i < N; i++) {
-        acc_post[k][i] += term[i];
-        d[k][i] *= gm[i];
-        s = __builtin_fmaf(d[k][i], m[i], s);
+        for (int i = 0; i < 4; i++) m[i] *= v.post;
+        gate_vec<KIND, 4>(a.scale, t, m, gate, gm, &b[k][4 * u], &acc_post[k][4 * u], dg);
+        if constexpr (TOKEN) pack_four<T>(out_g, u, dg);
+#pragma unroll
+        for (int i = 0; i < 4; i++) s = __builtin_fmaf(b[k][4 * u + i], m[i], s);
       }
+      packed(v.x[k]);
+      added(acc_post[k]);
+      if (n > 0 && a.dr != nullptr) store_vec<T, STREAM>(at_row<T>(a.dr, row, a.ld_dr, to[k]), out_r, n);
+      if constexpr (TOKEN)
+        if (n > 0 && a.dgate != nullptr) store_vec<T, STREAM>(at_row<T>(a.dgate, row, a.ld_dgate, to[k]), out_g, n);
     }
-    const float mean_post = group_sum(s, G, red) / (float)a.cols;
+    const float f = -(v.post * (group_sum_once(s, G, red[1]) * per_col));
     if (a.dx == nullptr) continue;
 #pragma unroll
     for (int k = 0; k < VPT; k++) {
-      const uint32_t c = (j + k * G) * N;
-      const int n = live ? inside<N>(c, a.cols) : 0;
-      if (n <= 0) continue;
+      const int n = row < a.rows ? N - sh[k] : 0;
       float m[N];
-      VecOf<T>::unpack(vx[k], m);
+      VecOf<T>::unpack(v.x[k], m);
 #pragma unroll
-      for (int i = 0; i < N; i++) m[i] = post * __builtin_fmaf(-(m[i] * post), mean_post, d[k][i]);
-      store_vec<T, STREAM>(static_cast<T*>(a.dx) + (int64_t)row * a.ld_dx + c, VecOf<T>::pack(m), n);
+      for (int i = 0; i < N; i++) m[i] = v.post * __builtin_fmaf(m[i], f, b[k][i]);
+      if (n > 0) store_vec<T, STREAM>(at_row<T>(a.dx, row, a.ld_dx, to[k]), VecOf<T>::pack(m), n);
     }
   }
-  // the groups of a workgroup add their sums in LDS, in order
-  for (int half = 0; half < 2; half++) {
-    float* part = half == 0 ? a.pre_part : a.post_part;
-    if (part == nullptr) continue;
+  auto leave = [&](const float (&acc)[VPT][N], float* part) {
+    if (part == nullptr) return;
     float* out = part + (int64_t)blockIdx.x * a.cols;
     if (groups == 1) {
 #pragma unroll
-      for (int k = 0; k < VPT; k++) {
-        const uint32_t c = (j + k * G) * N;
+      for (int k = 0; k < VPT; k++)
 #pragma unroll
-        for (int i = 0; i < N; i++)
-          if (c + i < a.cols) out[c + i] = half == 0 ? acc_pre[k][i] : acc_post[k][i];
-      }
-      continue;
+        for (int i = 0; i < N; i += 4) {
+          const uint32_t c = (j + k * G) * N + i;
+          if (c < a.cols) store_vec<float>(out + c, VecOf<float>::pack(&acc[k][i]), (int)(a.cols - c));
+        }
+      return;
     }
-    __syncthreads();  // the first half's sums are read
+    __syncthreads();  // the gains, or the other sums, are read
     for (int q = 0; q < groups; q++) {
       if (grp == q) {
 #pragma unroll
         for (int k = 0; k < VPT; k++)
 #pragma unroll
           for (int i = 0; i < N; i++) {
-            float* p = comb + (j + k * G) * N + i;
-            const float v = half == 0 ? acc_pre[k][i] : acc_post[k][i];
-            *p = q == 0 ? v : *p + v;
+            float* p = gains + (j + k * G) * N + i;
+            *p = q == 0 ? acc[k][i] : *p + acc[k][i];
           }
       }
       __syncthreads();
     }
-    for (uint32_t c = threadIdx.x; c < a.cols; c += blockDim.x) out[c] = comb[c];
-  }
+    for (uint32_t c = threadIdx.x; c < a.cols; c += blockDim.x) out[c] = gains[c];
+  };
+  leave(acc_pre, a.pre_part);
+  leave(acc_post, a.post_part);
 }
 
 // Wider rows: one workgroup a row at a time, read for each of its two sums and for its
 // outputs; the column sums stay in the workgroup's rows of the workspace (each lane adds
 // to its own columns).
-template <typename T>
+template <typename T, int KIND>
 __global__ __launch_bounds__(1024) void k_block_norms_back_wide(NormsBackArgs a) {
   constexpr int N = VecOf<T>::N;
   __shared__ float red[16];
@@ -416,8 +568,8 @@ __global__ __launch_bounds__(1024) void k_block_norms_back_wide(NormsBackArgs a)
       s += q;
     }
     const float mean_pre = group_sum(s, 1024, red) / (float)a.cols;
-    // t, m, d times gamma, its sum's term and dgate of one vector
-    auto form = [&](uint64_t c, float* t, float* m, float* d, float* term, float* dg) {
+    // t, m, b, d * m (added to sum) and dgate of one vector
+    auto form = [&](uint64_t c, float* t, float* m, float* b, float* sum, float* dg) {
       const int n = inside<N>(c, a.cols);
       float dy[N], h[N], gm[N];
       at(a.dy, a.ld_dy, c, dy);
@@ -425,29 +577,30 @@ __global__ __launch_bounds__(1024) void k_block_norms_back_wide(NormsBackArgs a)
       at(a.dh, a.ld_dh, c, t);
       at(a.x, a.ld_x, c, m);
       load_gamma<N>(a.pre, a.gamma_f32, (uint32_t)c, n, gm);
-      BackVec<T>::inner(t, dy, h, gm, pre, mean_pre);
+      back_vec<N>(t, dy, h, gm, pre, mean_pre);
       load_gamma<N>(a.post, a.gamma_f32, (uint32_t)c, n, gm);
 #pragma unroll
       for (int i = 0; i < N; i++) m[i] *= post;
-      const u32x4_t gate =
-          load_or_zero<T, false>(static_cast<const T*>(a.gate) + (int64_t)row * a.ld_gate + c, a.gate == nullptr ? 0 : n);
-      gate_vec<T>(a, t, m, gate, gm, d, term, dg);
+      float gate[N];
+      if constexpr (KIND != kNoGate) at(a.gate, a.ld_gate, c, gate);
+      if constexpr (KIND == kChannel)
 #pragma unroll
-      for (int i = 0; i < N; i++) d[i] *= gm[i];
+        for (int i = 0; i < N; i++) gate[i] = a.sigmoid ? sigmoid(gate[i]) : gate[i];
+      gate_vec<KIND, N>(a.scale, t, m, gate, gm, b, sum, dg);
     };
     s = 0.0f;
     for (uint64_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {
-      float t[N], m[N], d[N], term[N], dg[N], q = 0.0f;
-      form(c, t, m, d, term, dg);
+      float t[N], m[N], b[N], sum[N] = {}, dg[N], q = 0.0f;
+      form(c, t, m, b, sum, dg);
 #pragma unroll
-      for (int i = 0; i < N; i++) q = __builtin_fmaf(d[i], m[i], q);
+      for (int i = 0; i < N; i++) q = __builtin_fmaf(b[i], m[i], q);
       s += q;
     }
     const float mean_post = group_sum(s, 1024, red) / (float)a.cols;
     for (uint64_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {
       const int n = inside<N>(c, a.cols);
-      float t[N], m[N], d[N], term[N], dg[N], dy[N], h[N];
-      form(c, t, m, d, term, dg);
+      float t[N], m[N], b[N], sum[N] = {}, dg[N], dy[N], h[N];
+      form(c, t, m, b, sum, dg);
       at(a.dy, a.ld_dy, c, dy);
       at(a.h, a.ld_h, c, h);
       const bool first = row == blockIdx.x;
@@ -455,13 +608,14 @@ __global__ __launch_bounds__(1024) void k_block_norms_back_wide(NormsBackArgs a)
       for (int i = 0; i < N; i++) {
         if (i >= n) continue;
         if (out_pre != nullptr) out_pre[c + i] = __builtin_fmaf(dy[i], h[i] * pre, first ? 0.0f : out_pre[c + i]);
-        if (out_post != nullptr) out_post[c + i] = term[i] + (first ? 0.0f : out_post[c + i]);
+        if (out_post != nullptr) out_post[c + i] = sum[i] + (first ? 0.0f : out_post[c + i]);
       }
 #pragma unroll
-      for (int i = 0; i < N; i++) m[i] = post * __builtin_fmaf(-m[i], mean_post, d[i]);
+      for (int i = 0; i < N; i++) m[i] = post * __builtin_fmaf(-m[i], mean_post, b[i]);
       if (a.dr != nullptr) store_vec(static_cast<T*>(a.dr) + (int64_t)row * a.ld_dr + c, VecOf<T>::pack(t), n);
-      if (a.dgate != nullptr)
-        store_vec(static_cast<T*>(a.dgate) + (int64_t)row * a.ld_dgate + c, VecOf<T>::pack(dg), n);
+      if constexpr (KIND != kNoGate && KIND != kChannel)
+        if (a.dgate != nullptr)
+          store_vec(static_cast<T*>(a.dgate) + (int64_t)row * a.ld_dgate + c, VecOf<T>::pack(dg), n);
       if (a.dx != nullptr) store_vec(static_cast<T*>(a.dx) + (int64_t)row * a.ld_dx + c, VecOf<T>::pack(m), n);
     }
   }
@@ -481,9 +635,6 @@ struct SumArgs {
   uint32_t parts, cols;
   int dt_f32, gamma_f32, sigmoid;
 };
-__device__ __forceinline__ float one_of(const void* p, int f32, uint32_t c) {
-  return f32 ? static_cast<const float*>(p)[c] : VecOf<uint16_t>::one(static_cast<const uint16_t*>(p) + c);
-}
 constexpr int SLICES = 32;
 __global__ __launch_bounds__(SLICES * 32) void k_column_sums(SumArgs a) {
   __shared__ float part[SLICES][32];
@@ -540,30 +691,44 @@ struct BackShape {
 BackShape back_shape(int64_t rows, int64_t cols, int N) {
   BackShape b;
   b.row = row_shape((cols + N - 1) / N, 1);
-  if (b.row.vpt * N > 16) b.row = RowShape{0, 0};  // beyond the registers
+  if (b.row.vpt * N > 16 || cols < N) b.row = RowShape{0, 0};  // beyond the registers, or less than a vector
   if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
   b.groups = (int)std::min<int64_t>(std::max(1, 512 / b.row.G), rows);
-  b.parts = std::min((rows + b.groups - 1) / b.groups, 2 * kCus);
+  // the workgroups that a CU holds, by their registers: two of up to eight waves (twelve
+  // where a lane has four elements), or one
+  const int threads = b.row.G * b.groups;
+  const bool two = threads <= (b.row.vpt * N <= 4 ? 768 : 512);
+  b.parts = std::min((rows + b.groups - 1) / b.groups, two ? 2 * kCus : kCus);
   return b;
 }
 
-template <typename T>
+template <typename T, int KIND>
 hipError_t norms_back_t(const NormsBackArgs& a, const BackShape& b, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
-  if (b.row.vpt == 0) {
-    k_block_norms_back_wide<T><<<(unsigned)b.parts, 1024, 0, s>>>(a);
+  // the gains, and a gate that is one row for all; the groups' sums meet there
+  const int64_t lds = (int64_t)b.row.G * b.row.vpt * N * (KIND == kChannel ? 12 : 8);
+  if (b.row.vpt == 0 || lds > 150 * 1024) {
+    k_block_norms_back_wide<T, KIND><<<(unsigned)b.parts, 1024, 0, s>>>(a);
     return hipGetLastError();
   }
   const bool stream = (int64_t)a.rows * a.cols * 6 * (int64_t)sizeof(T) >= kStreamBytes;
-  const int lds = b.groups == 1 ? 0 : b.row.G * b.row.vpt * N * (int)sizeof(float);
+  hipError_t e = hipSuccess;
   with_vpt(b.row.vpt, [&](auto vpt) {
     constexpr int VPT = vpt.value * N <= 16 ? vpt.value : 1;  // what back_shape picks
-    if (stream)
-      k_block_norms_back<T, VPT, true><<<(unsigned)b.parts, b.groups * b.row.G, lds, s>>>(a, b.row.G);
-    else
-      k_block_norms_back<T, VPT, false><<<(unsigned)b.parts, b.groups * b.row.G, lds, s>>>(a, b.row.G);
+    auto* kernel = stream ? &k_block_norms_back<T, VPT, KIND, true, true> : &k_block_norms_back<T, VPT, KIND, false, true>;
+    if constexpr (VPT == 1)
+      if (b.row.G < 64) kernel = &k_block_norms_back<T, 1, KIND, false, false>;
+    if (lds > 64 * 1024)
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e == hipSuccess) kernel<<<(unsigned)b.parts, b.groups * b.row.G, lds, s>>>(a, b.row.G);
   });
-  return hipGetLastError();
+  return e == hipSuccess ? hipGetLastError() : e;
+}
+template <typename T>
+hipError_t norms_back_kind(const NormsBackArgs& a, const BackShape& b, bool shared, hipStream_t s) {
+  if (a.gate == nullptr) return norms_back_t<T, kNoGate>(a, b, s);
+  if (shared) return norms_back_t<T, kChannel>(a, b, s);
+  return a.sigmoid ? norms_back_t<T, kTokenSigmoid>(a, b, s) : norms_back_t<T, kToken>(a, b, s);
 }
 
 template <typename T, bool CODES>
@@ -629,8 +794,8 @@ hipError_t launch_block_norms_back(const void* dy, const void* dh, const void* h
     const NormsBackArgs a{dy,        dh,        h,     x,     gate,    post_gamma, pre_gamma,      post_rstd,
                           pre_rstd,  dx,        dresidual, shared ? nullptr : dgate, pre_part, post_part, ld_dy, ld_dh,
                           ld_h,      ld_x,      ld_gate, ld_dx, ld_dr, ld_dgate,   (uint32_t)rows, (uint32_t)cols,
-                          gamma_dt,  gate_act,  shared ? 1 : 0, scale};
-    const hipError_t e = dt == 0 ? norms_back_t<uint16_t>(a, b, s) : norms_back_t<float>(a, b, s);
+                          gamma_dt,  gate_act,  scale};
+    const hipError_t e = dt == 0 ? norms_back_kind<uint16_t>(a, b, shared, s) : norms_back_kind<float>(a, b, shared, s);
     if (e != hipSuccess) return e;
   } else if (sums) {  // no rows: the sums are zero (pointers only say which are asked for)
     pre_part = dpre_gamma;
