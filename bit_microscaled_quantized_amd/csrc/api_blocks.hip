@@ -64,7 +64,8 @@ nvfp4_status nvfp4_int8_quantize_gated(int act, const void* gate, const void* up
 
 nvfp4_status nvfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t* bytes) {
   if (bytes == nullptr) return NVFP4_EINVAL;
-  if (M < 0 || N < 1 || K < 16 || M >= (int64_t(1) << 24) || N >= (int64_t(1) << 24) || M * N >= (int64_t(1) << 37) ||
+  // M * N: the lanes of a launch, 256 for 64 x 64 sums, fit 32 bits
+  if (M < 0 || N < 1 || K < 16 || M >= (int64_t(1) << 24) || N >= (int64_t(1) << 24) || M * N > (int64_t(1) << 35) ||
       K > 131056 || K % 16 != 0)
     return NVFP4_ESHAPE;
   *bytes = nvfp4::int8_gemm_workspace(M, N, K);

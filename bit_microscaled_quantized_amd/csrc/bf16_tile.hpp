@@ -37,6 +37,11 @@
 // K and a stage's 64 count pairs, and a matrix instruction (32 x 32 x 32) reads the 16
 // bytes of a lane as 16 of them.
 //
+// With SHIFT, K along the rows (at least a stage) may end inside a stage and the stages
+// be of any number: the last stage is fetched as the K's last 64 values, and what of it
+// the stage before held is cleared in the first operand; an odd number is made even by a
+// stage that is all cleared.
+//
 // Addresses stay inside the operands: rows of a tile past the last are fetched
 // from the last row (or, KMAJOR, from the last 8 columns) and never used, and a
 // KMAJOR operand's values of k past its last from that one.  K along rows may end
@@ -118,11 +123,11 @@ struct TileFetch {
       }
     }
   }
-  // load j of stage kt
-  __device__ __forceinline__ void issue(const TileOperand& o, int kt, uint8_t* st, int wave, int j) const {
+  // load j of stage kt; not KMAJOR: that starts at value k of the rows
+  __device__ __forceinline__ void issue(const TileOperand& o, int kt, int k, uint8_t* st, int wave, int j) const {
     if constexpr (KMAJOR) kt = min(kt, (o.krows - 1) / TILE_K);
     const uint8_t* base = reinterpret_cast<const uint8_t*>(o.p) +
-                          (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)kt * TILE_K * 2);
+                          (KMAJOR ? (int64_t)kt * TILE_K * o.ld * 2 : (int64_t)k * 2);
     uint32_t v = off[j];
     if constexpr (KMAJOR)  // its row of k, at most the operand's last (64 rows stay within 32 bits, all need not)
       v += min(row0 + (uint32_t)(j * (8 / W)) * (o.ld * 2),
@@ -184,12 +189,21 @@ struct TileFrag {
   }
 };
 
+// Clears the first n chunks of every row of the first operand's stage.
+template <int W>
+__device__ __forceinline__ void tile_clear(uint8_t* st, int n) {
+  const int r = threadIdx.x;
+  if (r < tile_side(W))
+    for (int c = 0; c < n; c++)
+      *reinterpret_cast<u32x4_t*>(st + r * 128 + ((c ^ ((r >> 1) & 7)) << 4)) = u32x4_t{0, 0, 0, 0};
+}
+
 // acc = the product over the stages kt0 .. kt1 - 1 of K values of k.  EVEN: their
 // number is even and K a multiple of 64 (the caller's operands hold zeros up to
 // there); without it both operands have K along their rows.  All waves of the
 // workgroup take part; the caller's LDS stages are free again after its next
 // barrier.
-template <int W, bool AMAJ, bool BMAJ, bool EVEN, typename Op = MfmaBf16>
+template <int W, bool AMAJ, bool BMAJ, bool EVEN, typename Op = MfmaBf16, bool SHIFT = false>
 __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOperand& b, int K, int kt0, int kt1,
                                              uint8_t* lds, typename Op::Acc (&acc)[W][W]) {
   constexpr int OPERAND = tile_operand(W), STAGE = 2 * OPERAND;
@@ -199,6 +213,7 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
   TileFetch<W, AMAJ> fa;
   TileFetch<W, BMAJ> fb;
   static_assert(EVEN || (!AMAJ && !BMAJ), "odd stages are for K along rows");
+  static_assert(!SHIFT || (EVEN && !AMAJ && !BMAJ), "a shifted stage is for K along rows");
   static_assert(W > 1 || (!AMAJ && !BMAJ), "64 columns are too few for the transposing layout");
   fa.init(a, wave, lane);
   fb.init(b, wave, lane);
@@ -217,6 +232,10 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
   // The stage that ends past K, and one more where the rest is odd, go first,
   // each fetched and multiplied by itself.
   int first = kt0, end = kt1;
+  // where stage kt starts, and how many of its chunks are to be cleared
+  auto start = [&](int kt) { return SHIFT ? min(kt * TILE_K, K - TILE_K) : kt * TILE_K; };
+  auto excess = [&](int kt) { return kt >= kt1 ? 8 : max(0, (kt * TILE_K - (K - TILE_K)) / 8); };
+  if constexpr (SHIFT) end += (end - first) & 1;
   if constexpr (!EVEN) {
     auto alone = [&](int kt, bool ragged) {
       if (ragged) {
@@ -225,8 +244,8 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
       } else {
 #pragma unroll
         for (int j = 0; j < 2 * W; j++) {
-          fa.issue(a, kt, lds, wave, j);
-          fb.issue(b, kt, lds + OPERAND, wave, j);
+          fa.issue(a, kt, kt * TILE_K, lds, wave, j);
+          fb.issue(b, kt, kt * TILE_K, lds + OPERAND, wave, j);
         }
       }
       __builtin_amdgcn_s_waitcnt(0);
@@ -282,9 +301,9 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
 #define TILE_LOAD(kt, st, x)                             \
   do {                                                   \
     if ((x) & 1)                                         \
-      fb.issue(b, kt, (st) + OPERAND, wave, (x) >> 1);   \
+      fb.issue(b, kt, start(kt), (st) + OPERAND, wave, (x) >> 1); \
     else                                                 \
-      fa.issue(a, kt, st, wave, (x) >> 1);               \
+      fa.issue(a, kt, start(kt), st, wave, (x) >> 1);    \
   } while (0)
   // fragments q in use; the next step's from step rs of rst; loads x0 .. x0 + 2 W - 1 of stage kt into dst
 #define TILE_STEP(q, rst, rs, fetch, kt, dst, x0)                                                      \
@@ -323,12 +342,24 @@ __device__ __forceinline__ void tile_product(const TileOperand& a, const TileOpe
     __builtin_amdgcn_s_barrier();                                 \
     TILE_FENCE;                                                   \
     asm volatile("" ::: "memory");                                \
+    if constexpr (SHIFT) {                                        \
+      if (excess(k1) > 0) {                                       \
+        tile_clear<W>(nxt, excess(k1));                           \
+        __syncthreads();                                          \
+      }                                                           \
+    }                                                             \
     TILE_STEP(1, nxt, 0, true, k2, cur, 0);                       \
   } while (0)
 #pragma unroll
   for (int x = 0; x < 4 * W; x++) TILE_LOAD(first, lds, x);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
+  if constexpr (SHIFT) {
+    if (excess(first) > 0) {
+      tile_clear<W>(lds, excess(first));
+      __syncthreads();
+    }
+  }
 #pragma unroll
   for (int x = 0; x < 2 * W; x++) TILE_READ(lds, 0, 0, x);
 #pragma unroll
@@ -378,8 +409,8 @@ __device__ __forceinline__ void tile_product_short(const TileOperand& a, const T
     if (k > 0) __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2 * W; j++) {
-      fa.issue(a, k, lds, wave, j);
-      fb.issue(b, k, lds + tile_operand(W), wave, j);
+      fa.issue(a, k, k * TILE_K, lds, wave, j);
+      fb.issue(b, k, k * TILE_K, lds + tile_operand(W), wave, j);
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();

@@ -18,9 +18,11 @@ struct GemmArgs {
   const float* a_scales;
   const float* b_scales;
   void* c;
-  int* partial;  // null: whole tiles
+  int* partial;  // the parts' sums; null: no parts
   int64_t lda, ldb, ldc;
-  int M, N, K, parts;
+  int M, N, K;
+  int whole;  // tiles taken whole (int8_gemm.hip); the rest, and every block of int8_few.hip, in parts
+  int parts;
 };
 
 typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4), may_alias));

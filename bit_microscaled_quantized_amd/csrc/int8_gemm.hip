@@ -6,8 +6,9 @@
 // of the tiles do not show in the result.  Tiles are those of bf16_tile.hpp on the
 // 8-bit matrix instruction; the weight b is a tile's first operand, whose rows a lane
 // holds four in a row of (the output's columns), so that it stores pieces of four.
-// Where the tiles are few, K is split: parts leave their integers in the workspace,
-// in the order of the lanes, and a second launch adds and scales them.
+// Tiles that would leave most compute units idle in a round of their own (all of them, or
+// those behind the last full round) are split over K: the parts leave their integers in
+// the workspace, in the order of the lanes, and a second launch adds and scales them.
 #include "bf16_tile.hpp"
 #include "blocks_launch.hpp"
 #include "int8_device.hpp"
@@ -17,25 +18,45 @@ namespace nvfp4 {
 
 namespace {
 
-template <int W, bool EVEN, typename OutT>
+// Place of tile t: the whole ones, and the rest, each in tile_place's order among themselves.
+__device__ __forceinline__ void place(int t, int whole, int tiles, int num_n, int num_m, int& pn, int& pm) {
+  const int from = t < whole ? 0 : whole, count = t < whole ? whole : tiles - whole, bid = t - from;
+  const int xcd = bid & 7, per = count >> 3, rem = count & 7;
+  const int id = from + (xcd < rem ? xcd * (per + 1) : rem * (per + 1) + (xcd - rem) * per) + (bid >> 3);
+  const int width = 8 * num_m, first = id / width * 8, rows = min(num_n - first, 8);
+  pn = first + id % width % rows;
+  pm = id % width / rows;
+}
+
+// How a tile takes its stages: an even number of whole ones, any (SHIFT), or less than one.
+enum Stages { kEven, kAny, kOne };
+
+template <int W, int STAGES, typename OutT>
 __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_int8_tile(GemmArgs g) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int num_m = (g.M + TILE - 1) / TILE, num_n = (g.N + TILE - 1) / TILE, tiles = num_m * num_n;
-  const int part = blockIdx.x / tiles, t = blockIdx.x - part * tiles;
+  int t = blockIdx.x, part = 0, parts = 1;
+  if (t >= g.whole) {  // neighbours take different tiles' same part
+    const int rest = tiles - g.whole, u = t - g.whole;
+    parts = g.parts;
+    part = u / rest;
+    t = g.whole + u - part * rest;
+  }
   int pm, pn;
-  tile_place(t, num_n, num_m, pn, pm);
+  place(t, g.whole, tiles, num_n, num_m, pn, pm);
   const int m0 = pm * TILE, n0 = pn * TILE;
   const int KT = (g.K / 2 + TILE_K - 1) / TILE_K;
-  const int kt0 = (int)((int64_t)KT * part / g.parts), kt1 = (int)((int64_t)KT * (part + 1) / g.parts);
+  const int kt0 = (int)((int64_t)KT * part / parts), kt1 = (int)((int64_t)KT * (part + 1) / parts);
   const TileOperand wt{reinterpret_cast<const uint16_t*>(g.b + (int64_t)n0 * g.ldb), (uint32_t)(g.ldb / 2), g.N - n0, 0};
   const TileOperand tok{reinterpret_cast<const uint16_t*>(g.a + (int64_t)m0 * g.lda), (uint32_t)(g.lda / 2), g.M - m0, 0};
   intx16 acc[W][W];
-  tile_product<W, false, false, EVEN, MfmaInt8>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
+  tile_product<W, false, false, STAGES != kOne, MfmaInt8, STAGES == kAny>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, lr = lane & 31;
-  if (g.partial != nullptr) {
-    intx4* out = reinterpret_cast<intx4*>(g.partial) + (int64_t)blockIdx.x * (W * W * 4 * TILE_THREADS) + threadIdx.x;
+  if (parts > 1) {
+    intx4* out = reinterpret_cast<intx4*>(g.partial) + (int64_t)(blockIdx.x - g.whole) * (W * W * 4 * TILE_THREADS) +
+                 threadIdx.x;
 #pragma unroll
     for (int i = 0; i < W; i++)
 #pragma unroll
@@ -95,18 +116,18 @@ template <int W, typename OutT>
 __global__ __launch_bounds__(TILE_THREADS) void k_int8_join(GemmArgs g) {
   constexpr int TILE = tile_side(W), WAVE = 32 * W, PLANES = W * W * 4;
   const int num_m = (g.M + TILE - 1) / TILE, num_n = (g.N + TILE - 1) / TILE, tiles = num_m * num_n;
-  const int t = blockIdx.x / PLANES, plane = blockIdx.x % PLANES;
+  const int u = blockIdx.x / PLANES, plane = blockIdx.x % PLANES;
   int pm, pn;
-  tile_place(t, num_n, num_m, pn, pm);
+  place(g.whole + u, g.whole, tiles, num_n, num_m, pn, pm);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, lr = lane & 31;
   const int i = plane / (4 * W), j = plane / 4 % W, q = plane % 4;
   const int n = pn * TILE + (wave >> 1) * WAVE + 4 * h + 32 * i + 8 * q;
   const int m = pm * TILE + (wave & 1) * WAVE + lr + 32 * j;
   if (m >= g.M || n >= g.N) return;
-  const intx4* in = reinterpret_cast<const intx4*>(g.partial) + ((int64_t)t * PLANES + plane) * TILE_THREADS + threadIdx.x;
+  const intx4* in = reinterpret_cast<const intx4*>(g.partial) + ((int64_t)u * PLANES + plane) * TILE_THREADS + threadIdx.x;
   intx4 v{0, 0, 0, 0};
 #pragma unroll 4
-  for (int p = 0; p < g.parts; p++) v += in[(int64_t)p * tiles * PLANES * TILE_THREADS];
+  for (int p = 0; p < g.parts; p++) v += in[(int64_t)p * (tiles - g.whole) * PLANES * TILE_THREADS];
   float bs[4];
   four_scales(g, n, bs);
   store_four<OutT>(g, m, n, v, bs, g.a_scales[m]);
@@ -117,66 +138,79 @@ constexpr int64_t kFewTokens = 64;
 
 int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
 
-// Time of a product in microseconds on 256 CUs: one large tile a CU, two or four of the
-// smaller ones, in rounds.
+constexpr int64_t slots_of(int W) { return W == 4 ? 256 : W == 2 ? 512 : 1024; }  // workgroups on 256 CUs
+
+// Time of a round of `tiles` (at most slots_of(W)) of so many stages, in microseconds.  A
+// stage takes longer the more of them run: of a CU's own (small tiles), of the caches and
+// of the chip's power.
 double round_us(int64_t tiles, double stages, int W) {
-  const int64_t slots = W == 4 ? 256 : W == 2 ? 512 : 1024;
-  const double stage = W == 4 ? 1.55 : W == 2 ? 1.05 : 0.7, around = W == 4 ? 10.0 : 4.0;
-  return (double)((tiles + slots - 1) / slots) * (stages * stage + around);
+  const double full = (double)tiles / (double)slots_of(W);
+  if (W == 4) return stages * (1.2 + 0.35 * full) + 10.0;
+  if (W == 2) return stages * (0.62 + 0.4 * full) + 6.0;
+  return stages * (0.4 + 0.6 * full) + 4.0;
 }
 
 struct Plan {
   int W, parts;
-  int64_t tiles, bytes;
+  int64_t tiles, whole, bytes;
 };
+double plan_us(const Plan& p, int64_t stages) {
+  const int64_t rest = p.tiles - p.whole, slots = slots_of(p.W);
+  double us = (double)(p.whole / slots) * round_us(slots, (double)stages, p.W);
+  if (p.whole % slots > 0) us += round_us(p.whole % slots, (double)stages, p.W);
+  if (rest > 0)  // and a launch that reads the parts' sums
+    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W) + 3.0 + (double)p.bytes * 2.0 / 6.0e6;
+  return us;
+}
 // split false: whole tiles only
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool split) {
   const int64_t stages = (K / 2 + TILE_K - 1) / TILE_K;
-  Plan best{4, 1, tiles_of(M, 4) * tiles_of(N, 4), 0};
-  double best_us = 1e300;
+  Plan best{0, 1, 0, 0, 0};
+  double best_us = 0;
   for (int W : {4, 2, 1}) {
-    const int64_t tiles = tiles_of(M, W) * tiles_of(N, W), slots = W == 4 ? 256 : W == 2 ? 512 : 1024;
-    if (tiles > (int64_t(1) << 22)) continue;  // the lanes of a launch fit 32 bits
-    const int64_t most = split ? std::max<int64_t>(1, std::min<int64_t>(slots / tiles, stages / 4)) : 1;
-    for (int64_t parts = 1; parts <= most; parts++) {
-      const int64_t bytes = parts == 1 ? 0 : parts * tiles * tile_side(W) * tile_side(W) * 4;
-      const double us = round_us(tiles * parts, (double)((stages + parts - 1) / parts), W) +
-                        (parts == 1 ? 0.0 : 3.0 + (double)bytes * 2.0 / 4.5e6);
-      if (us < best_us * 0.99) {
-        best_us = us;
-        best = Plan{W, (int)parts, tiles, bytes};
-      }
-    }
+    if (K < 2 * TILE_K && W > 1) continue;
+    const int64_t tiles = tiles_of(M, W) * tiles_of(N, W), slots = slots_of(W);
+    auto weigh = [&](const Plan& p) {
+      const double us = plan_us(p, stages);
+      if (best.W == 0 || us < best_us * 0.99) best = p, best_us = us;
+    };
+    weigh(Plan{W, 1, tiles, tiles, 0});
+    const int64_t whole = tiles / slots * slots, rest = tiles - whole;
+    if (!split || rest == 0) continue;
+    const int64_t most = std::min(slots / rest, stages / 4);
+    for (int64_t parts = 2; parts <= most; parts++)
+      weigh(Plan{W, (int)parts, tiles, whole, parts * rest * tile_side(W) * tile_side(W) * 4});
   }
   return best;
 }
 
-template <int W, bool EVEN, typename OutT>
-hipError_t allow_tile() {
-  static std::atomic<uint64_t> done{0};
-  if (tile_lds(W) <= 64 * 1024) return hipSuccess;
-  return once_per_device(done, [] {
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_int8_tile<W, EVEN, OutT>),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds(W));
-  });
+template <int W, int STAGES, typename OutT>
+hipError_t tile_go(const GemmArgs& g, unsigned grid, hipStream_t s) {
+  if (tile_lds(W) > 64 * 1024) {
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = once_per_device(done, [] {
+      return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_int8_tile<W, STAGES, OutT>),
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds(W));
+    });
+    if (e != hipSuccess) return e;
+  }
+  k_int8_tile<W, STAGES, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
+  return hipGetLastError();
 }
 
 template <int W, typename OutT>
 hipError_t gemm_w(const GemmArgs& g, const Plan& p, hipStream_t s) {
-  const unsigned grid = (unsigned)(p.tiles * p.parts);
-  // a whole number of pairs of stages for every part
-  const bool even = g.K % (4 * TILE_K) == 0 && p.parts == 1;
+  const int64_t rest = p.tiles - p.whole;
+  const unsigned grid = (unsigned)(p.whole + rest * p.parts);
   hipError_t e;
-  if (even) {
-    e = allow_tile<W, true, OutT>();
-    if (e == hipSuccess) k_int8_tile<W, true, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
-  } else {
-    e = allow_tile<W, false, OutT>();
-    if (e == hipSuccess) k_int8_tile<W, false, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
-  }
-  if (e == hipSuccess) e = hipGetLastError();
-  if (e != hipSuccess || p.parts == 1) return e;
-  k_int8_join<W, OutT><<<(unsigned)(p.tiles * W * W * 4), TILE_THREADS, 0, s>>>(g);
+  if (g.K % (4 * TILE_K) == 0 && rest == 0)
+    e = tile_go<W, kEven, OutT>(g, grid, s);
+  else if (W > 1 || g.K >= 2 * TILE_K)
+    e = tile_go<W, kAny, OutT>(g, grid, s);
+  else
+    e = tile_go<1, kOne, OutT>(g, grid, s);
+  if (e != hipSuccess || rest == 0) return e;
+  k_int8_join<W, OutT><<<(unsigned)(rest * W * W * 4), TILE_THREADS, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -199,16 +233,14 @@ hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, in
   if (M <= kFewTokens) {
     const FewPlan f = few_plan(M, N, K);
     const bool split = f.parts > 1 && workspace != nullptr && workspace_bytes >= f.bytes;
-    const GemmArgs g{a,   b,   a_scales, b_scales, c,      split ? static_cast<int*>(workspace) : nullptr,
-                     lda, ldb, ldc,      (int)M,   (int)N, (int)K,
-                     split ? f.parts : 1};
+    const GemmArgs g{a,   b,   a_scales, b_scales, c, split ? static_cast<int*>(workspace) : nullptr,
+                     lda, ldb, ldc, (int)M, (int)N, (int)K, 0, split ? f.parts : 1};
     return int8_few(g, c_dt, s);
   }
   Plan p = plan_of(M, N, K, true);
   if (workspace == nullptr || workspace_bytes < p.bytes) p = plan_of(M, N, K, false);
-  const GemmArgs g{a,   b,   a_scales, b_scales, c,      p.parts > 1 ? static_cast<int*>(workspace) : nullptr,
-                   lda, ldb, ldc,      (int)M,   (int)N, (int)K,
-                   p.parts};
+  const GemmArgs g{a,   b,   a_scales, b_scales, c, static_cast<int*>(workspace),
+                   lda, ldb, ldc, (int)M, (int)N, (int)K, (int)p.whole, p.parts};
   return c_dt == 0 ? gemm_t<uint16_t>(g, p, s) : gemm_t<float>(g, p, s);
 }
 

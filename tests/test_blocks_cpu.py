@@ -61,7 +61,7 @@ def gemm(**kw):
     (dict(c_dt=2), E),
     (dict(M=-1), S), (dict(N=0), S), (dict(K=0), S), (dict(K=8), S), (dict(K=72, lda=80, ldb=80), S),
     (dict(K=131072, lda=131072, ldb=131072), S),  # 128 * 128 * K reaches 2^31
-    (dict(M=1 << 24), S), (dict(N=1 << 24, ldc=1 << 24), S), (dict(M=1 << 20, N=1 << 17, ldc=1 << 17), S),
+    (dict(M=1 << 24), S), (dict(N=1 << 24, ldc=1 << 24), S), (dict(M=1 << 20, N=(1 << 15) + 1, ldc=1 << 17), S),
     (dict(lda=48), S), (dict(ldb=48), S), (dict(ldc=39), S), (dict(lda=1 << 23), S), (dict(ldb=1 << 23), S),
     (dict(ldc=HUGE), S),
     (dict(lda=72), A), (dict(ldb=72), A), (dict(a=FAKE + 8), A), (dict(b=FAKE + 8), A), (dict(a_scales=FAKE + 2), A),
@@ -75,8 +75,9 @@ def test_int8_gemm_arguments(kw, status):
 def test_int8_gemm_workspace():
     size = nv.nvfp4_int8_gemm_workspace_size
     assert size(0, 5, 16) == 0 and size(8192, 20480, 5120) == 0
-    for M, N, K in ((1, 1, 16), (17, 20480, 5120), (300, 513, 131056), ((1 << 24) - 1, 1, 16), (1, (1 << 24) - 1, 16)):
-        assert 0 <= size(M, N, K) <= 1 << 30 and size(M, N, K) % 16 == 0
+    for M, N, K in ((1, 1, 16), (17, 20480, 5120), (300, 513, 131056), ((1 << 24) - 1, 1, 16), (1, (1 << 24) - 1, 16),
+                    (1 << 20, 1 << 15, 16), (1 << 20, 1 << 15, 131056)):
+        assert 0 <= size(M, N, K) <= 1 << 28 and size(M, N, K) % 16 == 0
     out = ctypes.c_int64(-7)
     f = b.load_library().nvfp4_int8_gemm_workspace_size
     assert f(4, 4, 17, ctypes.byref(out)) == S and out.value == -7
