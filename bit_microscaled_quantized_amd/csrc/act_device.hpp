@@ -60,31 +60,11 @@ void with_act(int act, F&& f) {
   }
 }
 
-// Eight consecutive elements of a row (n of them inside it, n <= 0: none; the rest zero).
+// A vector of a row (n of its elements inside it, n <= 0: none; the rest zero).
 template <typename T, bool STREAM>
-struct Eight {
-  static constexpr int V = 8 / VecOf<T>::N;  // 16-byte vectors
-  u32x4_t v[V];
-  __device__ __forceinline__ void load(const T* p, int n) {
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int m = n - i * VecOf<T>::N;
-      v[i] = u32x4_t{0, 0, 0, 0};
-      if (m > 0) v[i] = load_vec<T, STREAM>(p + i * VecOf<T>::N, m);
-    }
-  }
-  __device__ __forceinline__ void unpack(float* f) const {
-#pragma unroll
-    for (int i = 0; i < V; i++) VecOf<T>::unpack(v[i], f + i * VecOf<T>::N);
-  }
-  static __device__ __forceinline__ void store(T* p, const float* f, int n) {
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int m = n - i * VecOf<T>::N;
-      if (m > 0) store_vec<T, STREAM>(p + i * VecOf<T>::N, VecOf<T>::pack(f + i * VecOf<T>::N), m);
-    }
-  }
-};
+__device__ __forceinline__ u32x4_t load_or_zero(const T* p, int n) {
+  return n > 0 ? load_vec<T, STREAM>(p, n) : u32x4_t{0, 0, 0, 0};
+}
 
 // The low bytes of four integers held as 1.5 * 2^23 + integer, in order.
 __device__ __forceinline__ uint32_t bytes_of(float a, float b, float c, float d) {

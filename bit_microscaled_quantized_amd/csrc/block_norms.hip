@@ -54,11 +54,6 @@ __device__ __forceinline__ T* at_row(P* p, uint32_t row, int64_t ld, uint32_t of
     return reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(start) + off);
 }
 
-template <typename T, bool STREAM>
-__device__ __forceinline__ u32x4_t load_or_zero(const T* p, int n) {
-  return n > 0 ? load_vec<T, STREAM>(p, n) : u32x4_t{0, 0, 0, 0};
-}
-
 // f becomes h: residual + scale * (g * ((x * rstd) * gamma)); elements past the row's end stay 0
 template <typename T>
 __device__ __forceinline__ void sum_vec(const NormsArgs& a, float* f, u32x4_t r, u32x4_t gate, float rstd, uint32_t c,
@@ -413,13 +408,21 @@ __global__ __launch_bounds__(1024, 4) void k_block_norms_back(NormsBackArgs a, i
   const float per_col = 1.0f / (float)a.cols;
   NormsRow<VPT> next;
   if constexpr (AHEAD) load(blockIdx.x * groups, next);
-  for (uint32_t c = threadIdx.x; c < width; c += blockDim.x) {
-    const bool in = c < a.cols;
-    gains[c] = in ? one_of(a.pre, a.gamma_f32, c) : 0.0f;
-    gains[width + c] = in ? one_of(a.post, a.gamma_f32, c) : 0.0f;
+#pragma unroll 2
+  for (uint32_t c = threadIdx.x * 4; c < width; c += blockDim.x * 4) {
+    const int n = inside<4>(c, a.cols);
+    float pre[4] = {}, post[4] = {}, gate[4] = {};
+    if (n > 0) {
+      load_gamma<4>(a.pre, a.gamma_f32, c, n, pre);
+      load_gamma<4>(a.post, a.gamma_f32, c, n, post);
+      if constexpr (KIND == kChannel) load_gamma<4>(a.gate, sizeof(T) == 4, c, n, gate);
+    }
+    *reinterpret_cast<u32x4_t*>(gains + c) = VecOf<float>::pack(pre);
+    *reinterpret_cast<u32x4_t*>(gains + width + c) = VecOf<float>::pack(post);
     if constexpr (KIND == kChannel) {
-      const float g = in ? one_of(a.gate, sizeof(T) == 4, c) : 0.0f;
-      gains[2 * width + c] = a.sigmoid ? sigmoid(g) : g;
+#pragma unroll
+      for (int i = 0; i < 4; i++) gate[i] = a.sigmoid ? sigmoid(gate[i]) : gate[i];
+      *reinterpret_cast<u32x4_t*>(gains + 2 * width + c) = VecOf<float>::pack(gate);
     }
   }
   __syncthreads();

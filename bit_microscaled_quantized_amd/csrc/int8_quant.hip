@@ -21,15 +21,15 @@ struct QuantArgs {
   uint32_t rows, cols, padded;  // padded: cols up to a multiple of 16
 };
 
-// v of eight elements
-template <typename T, int ACT, bool STREAM>
-__device__ __forceinline__ void values_of(const QuantArgs& a, const Eight<T, STREAM>& g, const Eight<T, STREAM>& u,
-                                          float* f) {
-  g.unpack(f);
-  float fu[8];
-  if (a.up != nullptr) u.unpack(fu);
+// v of a vector's elements
+template <typename T, int ACT>
+__device__ __forceinline__ void values_of(const QuantArgs& a, u32x4_t g, u32x4_t u, float* f) {
+  constexpr int N = VecOf<T>::N;
+  float fu[N];
+  VecOf<T>::unpack(g, f);
+  VecOf<T>::unpack(u, fu);
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
+  for (int i = 0; i < N; i++) {
     f[i] = act_of<ACT>(f[i]);
     if (a.up != nullptr) f[i] *= fu[i];
   }
@@ -37,25 +37,26 @@ __device__ __forceinline__ void values_of(const QuantArgs& a, const Eight<T, STR
 
 template <typename T, int ACT, int VPT, bool STREAM>
 __global__ __launch_bounds__(1024) void k_int8_rows(QuantArgs a, int G) {
+  constexpr int N = VecOf<T>::N;
   __shared__ uint32_t red[16];
   const uint32_t row = blockIdx.x * (blockDim.x / G) + threadIdx.x / G, j = threadIdx.x % G;
   const bool live = row < a.rows;
   const T* gr = static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g;
   const T* ur = static_cast<const T*>(a.up) + (int64_t)row * a.ld_u;
-  Eight<T, STREAM> g[VPT], u[VPT];
+  u32x4_t g[VPT], u[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
-    const uint32_t c = (j + k * G) * 8;
-    const int n = live && c < a.cols ? (int)min(a.cols - c, 8u) : 0;
-    g[k].load(gr + c, n);
-    if (a.up != nullptr) u[k].load(ur + c, n);
+    const uint32_t c = (j + k * G) * N;
+    const int n = live && c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
+    g[k] = load_or_zero<T, STREAM>(gr + c, n);
+    u[k] = load_or_zero<T, STREAM>(ur + c, a.up == nullptr ? 0 : n);
   }
-  float f[VPT][8];
+  float f[VPT][N];
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
-    values_of<T, ACT, STREAM>(a, g[k], u[k], f[k]);  // zeros past the row's end
-    m = most_of<8>(f[k], m);
+    values_of<T, ACT>(a, g[k], u[k], f[k]);  // zeros past the row's end
+    m = most_of<N>(f[k], m);
   }
   const RowCode q(group_max(m, G, red));
   if (!live) return;
@@ -63,44 +64,43 @@ __global__ __launch_bounds__(1024) void k_int8_rows(QuantArgs a, int G) {
   int8_t* out = a.codes + (int64_t)row * a.ld_codes;
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
-    const uint32_t c = (j + k * G) * 8;
-    if (c < a.padded) store_codes<8>(q, f[k], out, c);
+    const uint32_t c = (j + k * G) * N;
+    if (c < a.padded) store_codes<N>(q, f[k], out, c);
   }
 }
 
 // Wider rows: one workgroup a row.
 template <typename T, int ACT>
 __global__ __launch_bounds__(1024) void k_int8_wide(QuantArgs a) {
+  constexpr int N = VecOf<T>::N;
   __shared__ uint32_t red[16];
   const uint32_t row = blockIdx.x;
   const T* gr = static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g;
   const T* ur = static_cast<const T*>(a.up) + (int64_t)row * a.ld_u;
-  auto at = [&](uint64_t c, float* f) {
-    const int n = c < a.cols ? (int)min((uint64_t)8, a.cols - c) : 0;
-    Eight<T, false> g, u;
-    g.load(gr + c, n);
-    if (a.up != nullptr) u.load(ur + c, n);
-    values_of<T, ACT, false>(a, g, u, f);
+  auto at = [&](uint32_t c, float* f) {
+    const int n = c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
+    values_of<T, ACT>(a, load_or_zero<T, false>(gr + c, n), load_or_zero<T, false>(ur + c, a.up == nullptr ? 0 : n), f);
   };
   uint32_t m = 0;
-  for (uint64_t c = threadIdx.x * 8; c < a.cols; c += 1024 * 8) {
-    float f[8];
+  for (uint32_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {  // fewer than 2^31 columns
+    float f[N];
     at(c, f);
-    m = most_of<8>(f, m);
+    m = most_of<N>(f, m);
   }
   const RowCode q(group_max(m, 1024, red));
   if (threadIdx.x == 0) a.scales[row] = q.scale;
   int8_t* out = a.codes + (int64_t)row * a.ld_codes;
-  for (uint64_t c = threadIdx.x * 8; c < a.padded; c += 1024 * 8) {
-    float f[8];
+  for (uint32_t c = threadIdx.x * N; c < a.padded; c += 1024 * N) {
+    float f[N];
     at(c, f);
-    *reinterpret_cast<u32x2_t*>(out + c) = u32x2_t{q.four(f), q.four(f + 4)};
+    store_codes<N>(q, f, out, c);
   }
 }
 
+// Two vectors a lane stream best, one finishes a few rows soonest.
 template <typename T, int ACT>
 hipError_t quantize_t(const QuantArgs& a, hipStream_t s) {
-  const int64_t vecs = a.padded / 8;
+  const int64_t vecs = a.padded / VecOf<T>::N;
   const RowShape r = row_shape(vecs, a.rows >= 1024 && vecs > 128 ? 2 : 1);
   if (r.vpt == 0 || r.vpt > 5) {
     k_int8_wide<T, ACT><<<a.rows, 1024, 0, s>>>(a);
