@@ -240,16 +240,17 @@ hipError_t few(const GemmArgs& g, hipStream_t s) {
 
 }  // namespace
 
-// K is split over workgroups until there are 640 of four waves that share tokens, with two stages
-// or more (20480 x 5120 in two parts, 5120 x 20480 in eight, 1024 x 5120 in ten); waves on
-// their own, 5120 in all with two stages, where they would have eight or more (a token
-// of 5120 x 20480 20.7 us in four parts, 28 in one).
+// K is split over workgroups until there are two on each of 256 CUs of those that share tokens
+// (48 tokens of 5120 x 20480 26.9 us in six parts, 28.4 in eight; 32 tokens of 20480 x 5120, 320
+// workgroups already, 26.3 in two, 27.3 in one, but 48 level), with two stages or more;
+// waves on their own, 5120 in all with two stages, where they would have eight or more (a
+// token of 5120 x 20480 20.7 us in four parts, 28 in one).
 FewPlan few_plan(int64_t M, int64_t N, int64_t K) {
   const Shape f = shape_of(M, N, K);
   const int64_t blocks = (N + 16 * f.rg - 1) / (16 * f.rg), stages = (K + STAGE - 1) / STAGE;
   int64_t parts = 1;
   if (f.rg > 1)
-    parts = std::min(640 / blocks, stages / 2);
+    parts = std::min((blocks > 256 && M <= 32 ? 640 : 512) / blocks, stages / 2);
   else if (stages >= 8 * f.kw)
     parts = std::min(5120 / (blocks * f.kw), stages / (2 * f.kw));
   parts = std::max<int64_t>(parts, 1);
