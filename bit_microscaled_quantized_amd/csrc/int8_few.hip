@@ -40,13 +40,13 @@ __device__ __forceinline__ int slot(int r, int c) { return r * STAGE + ((c ^ (r 
 template <int MT, int RG, int KW, typename OutT>
 __global__ __launch_bounds__(64 * RG * KW) void k_int8_few(GemmArgs g) {
   constexpr bool SHARED = RG > 1;
-  constexpr int TOK = SHARED ? 16 * MT * STAGE : 0;  // a slice's buffer of tokens
+  static_assert(RG == 1 || (RG == 4 && KW == 1), "a row of 16 chunks of tokens to 16 threads");
+  constexpr int TOK = SHARED ? 16 * MT * STAGE : 0;  // a buffer of tokens
   extern __shared__ __align__(16) int8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rg = wave % RG, kw = wave / RG;
-  int8_t* tok = lds + kw * (2 * TOK);
-  int8_t* own = lds + KW * (2 * TOK) + wave * (16 * STAGE);
+  int8_t* own = lds + 2 * TOK + wave * (16 * STAGE);
   const int blocks = (g.N + 16 * RG - 1) / (16 * RG);
   const int part = blockIdx.x / blocks, block = blockIdx.x - part * blocks;
   const int n0 = (block * RG + rg) * 16;
@@ -59,50 +59,48 @@ __global__ __launch_bounds__(64 * RG * KW) void k_int8_few(GemmArgs g) {
   const int8_t* base = g.b + (int64_t)nb * g.ldb;
   uint32_t ob[2];
 #pragma unroll
-  for (int j = 0; j < 2; j++)
-    ob[j] = (uint32_t)min(8 * j + (lane >> 3), g.N - 1 - nb) * (uint32_t)g.ldb + 16 * (lane & 7);
-  // tokens: own fragments, or a lane's share of a slice's stage, chunk l % 16 of rows l / 16
-  // + 4 RG t of its RG waves
-  const int sl = rg * 64 + lane;
-  constexpr int TA = SHARED ? 4 * MT / RG : MT;
+  for (int j = 0; j < 2; j++) ob[j] = (uint32_t)min(8 * j + (lane >> 3), g.N - 1 - nb) * (uint32_t)g.ldb;
+  // tokens: own fragments, or a lane's share of a stage, chunk tid % 16 of rows tid / 16 + 16 t
+  constexpr int TA = MT;
   uint32_t oa[TA];
 #pragma unroll
-  for (int t = 0; t < TA; t++)
-    oa[t] = SHARED ? (uint32_t)min(4 * RG * t + (sl >> 4), g.M - 1) * (uint32_t)g.lda + 16 * (sl & 15)
-                   : (uint32_t)min(16 * t + i, g.M - 1) * (uint32_t)g.lda + 16 * q;
+  for (int t = 0; t < TA; t++) oa[t] = (uint32_t)min(16 * t + (SHARED ? tid >> 4 : i), g.M - 1) * (uint32_t)g.lda;
   intx4 acc[MT], vb[4], va[SHARED ? TA : 4 * TA];
 #pragma unroll
   for (int t = 0; t < MT; t++) acc[t] = intx4{0, 0, 0, 0};
-  // loads of stage kt; the last one may end inside it, and zeros follow K
-  auto load_b = [&](int kt) {
-    const int8_t* p = base + STAGE * kt;
-    if (kt >= end) return;
-    if (STAGE * (kt + 1) <= g.K) {
-#pragma unroll
-      for (int j = 0; j < 4; j++) vb[j] = load16<true>(p + 128 * (j >> 1), ob[j & 1]);
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      vb[j] = intx4{0, 0, 0, 0};
-      if (STAGE * kt + 128 * (j >> 1) + 16 * (lane & 7) < g.K) vb[j] = load16<true>(p + 128 * (j >> 1), ob[j & 1]);
-    }
+  // Loads of stage kt.  The last one may end inside: its last chunk stands for those past K,
+  // and the weight's are cleared as they are put into LDS.  Waves that share tokens load on no
+  // condition, behind their slice's end all lanes from one place, so that the compiler waits for
+  // a stage with the next one's loads in flight (48 tokens of 20480 x 5120 28.8 against
+  // 30.1 us; a stage more in flight gained nothing).  Waves on their own hide each
+  // other's waits (131072 x 5120 96 us, 99 with loads on no condition).
+  auto offset = [&](uint32_t row, int kt, int col) {
+    return !SHARED || kt < end ? row + (uint32_t)min(STAGE * kt + col, g.K - 16) : 0u;
   };
-  // codes of tokens past K meet zeros of the weight: any will do, of a place inside the row
+  auto load_b = [&](int kt) {
+    if (!SHARED && kt >= end) return;
+#pragma unroll
+    for (int j = 0; j < 4; j++) vb[j] = load16<true>(base, offset(ob[j & 1], kt, 128 * (j >> 1) + 16 * (lane & 7)));
+  };
+  auto put_b = [&](int kt) {
+    if (STAGE * (kt + 1) > g.K) {
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (STAGE * kt + 128 * (j >> 1) + 16 * (lane & 7) >= g.K) vb[j] = intx4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      *reinterpret_cast<intx4*>(own + slot(8 * (j & 1) + (lane >> 3), 8 * (j >> 1) + (lane & 7))) = vb[j];
+  };
   auto load_a = [&](int kt) {
-    const int8_t* p = g.a + STAGE * kt;
-    if (kt >= end) return;
-    const int left = g.K - STAGE * kt;
-    if constexpr (SHARED) {
-      const uint32_t back = 16 * (sl & 15) < left ? 0 : 16 * (sl & 15);
+    if (!SHARED && kt >= end) return;
 #pragma unroll
-      for (int t = 0; t < TA; t++) va[t] = load16<false>(p, oa[t] - back);
-    } else {
+    for (int t = 0; t < TA; t++) {
+      if constexpr (SHARED) {
+        va[t] = load16<false>(g.a, offset(oa[t], kt, 16 * (tid & 15)));
+      } else {
 #pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const uint32_t on = 64 * s + 16 * q < left ? 64 * s : 0u - 16 * q;
-#pragma unroll
-        for (int t = 0; t < TA; t++) va[s * TA + t] = load16<false>(p, oa[t] + on);
+        for (int s = 0; s < 4; s++) va[s * TA + t] = load16<false>(g.a, offset(oa[t], kt, 64 * s + 16 * q));
       }
     }
   };
@@ -110,7 +108,7 @@ __global__ __launch_bounds__(64 * RG * KW) void k_int8_few(GemmArgs g) {
     if constexpr (SHARED) {
 #pragma unroll
       for (int t = 0; t < TA; t++)
-        *reinterpret_cast<intx4*>(tok + buf * TOK + slot(4 * RG * t + (sl >> 4), sl & 15)) = va[t];
+        *reinterpret_cast<intx4*>(lds + buf * TOK + slot(16 * t + (tid >> 4), tid & 15)) = va[t];
     }
   };
   load_a(first);
@@ -120,18 +118,9 @@ __global__ __launch_bounds__(64 * RG * KW) void k_int8_few(GemmArgs g) {
     load_a(first + 1);
     __syncthreads();
   }
-  // every wave of a workgroup takes as many steps, where they meet at barriers (slices
-  // differ by one stage at most)
-  const int steps = SHARED && KW > 1 ? (stages + slices - 1) / slices : end - first;
-  for (int n = 0; n < steps; n++) {
-    const int kt = first + n, buf = n & 1;
-    if (SHARED && KW > 1 && kt >= end) {
-      __syncthreads();
-      break;
-    }
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      *reinterpret_cast<intx4*>(own + slot(8 * (j & 1) + (lane >> 3), 8 * (j >> 1) + (lane & 7))) = vb[j];
+  for (int kt = first; kt < end; kt++) {
+    const int buf = (kt - first) & 1;
+    put_b(kt);
     load_b(kt + 1);
     if constexpr (SHARED) {
       put_a(buf ^ 1);
@@ -144,7 +133,7 @@ __global__ __launch_bounds__(64 * RG * KW) void k_int8_few(GemmArgs g) {
       for (int t = 0; t < MT; t++) {
         intx4 fa;
         if constexpr (SHARED)
-          fa = *reinterpret_cast<const intx4*>(tok + buf * TOK + slot(16 * t + i, 4 * s + q));
+          fa = *reinterpret_cast<const intx4*>(lds + buf * TOK + slot(16 * t + i, 4 * s + q));
         else
           fa = va[s * TA + t];
         acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb, fa, acc[t], 0, 0, 0);
@@ -203,7 +192,7 @@ __global__ __launch_bounds__(64 * RG) void k_int8_few_join(GemmArgs g) {
 
 template <int MT, int RG, int KW, typename OutT>
 hipError_t few_t(const GemmArgs& g, hipStream_t s) {
-  constexpr int LDS = RG * KW * 16 * STAGE + (RG > 1 ? KW * 2 * 16 * MT * STAGE : 0);
+  constexpr int LDS = RG * KW * 16 * STAGE + (RG > 1 ? 2 * 16 * MT * STAGE : 0);
   static_assert(LDS <= 64 * 1024 && KW * RG * MT * 1024 <= LDS, "LDS of a workgroup");
   const unsigned blocks = (unsigned)((g.N + 16 * RG - 1) / (16 * RG));
   k_int8_few<MT, RG, KW, OutT><<<blocks * g.parts, 64 * RG * KW, LDS, s>>>(g);
