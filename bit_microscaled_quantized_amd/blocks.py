@@ -328,6 +328,7 @@ def block_norms_int8(x, residual, post_gamma, pre_gamma, gate=None, scale: float
 
 def int8_matmul(codes, scales, w_codes, w_scales, dtype=torch.bfloat16):
     """codes w_codes^T times their scales: [rows, out] of the given type."""
+    _no_grad(scales, w_scales)
     _on_gpu(codes, scales, w_codes, w_scales)
     if codes.dim() != 2 or w_codes.dim() != 2 or codes.shape[1] != w_codes.shape[1] or codes.shape[1] % 16 != 0 \
             or codes.shape[1] == 0:
@@ -373,6 +374,13 @@ class Int8Linear(torch.nn.Module):
         if getattr(layer, "bias", None) is not None:
             raise ValueError("Int8Linear has no bias")
         return cls(layer.weight)
+
+    def _apply(self, fn, recurse=True):
+        scales = self.scales
+        super()._apply(fn, recurse)
+        if self.scales.dtype != torch.float32:  # a change of the model's type leaves the scales in FP32
+            self.scales = scales.to(self.scales.device)
+        return self
 
     def _inputs(self, x):
         if x.dim() == 0 or x.shape[-1] != self.in_features:

@@ -20,7 +20,8 @@ __device__ __forceinline__ float sigmoid(float v) {
 enum Act { kNone = 0, kSilu = 1, kGelu = 2, kRelu2 = 3 };
 
 // act(v); with SLOPE its derivative as well.  GELU's (1 + tanh t) / 2 is the logistic
-// function of 2 t.
+// function p of 2 t; where v^2 overflows its slope is p, whose other term holds 1 - p or a
+// of 0: v^2 is bounded, so that the term is 0 and not 0 times infinity.
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ float act_of(float v, float& slope) {
   if constexpr (ACT == kSilu) {
@@ -31,7 +32,8 @@ __device__ __forceinline__ float act_of(float v, float& slope) {
     constexpr float C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float q = v * v;
     const float p = sigmoid(v * __builtin_fmaf(q, C * 0.044715f, C)), a = v * p;
-    if constexpr (SLOPE) slope = __builtin_fmaf(a * (1.0f - p), __builtin_fmaf(q, 3.0f * C * 0.044715f, C), p);
+    if constexpr (SLOPE)
+      slope = __builtin_fmaf(a * (1.0f - p), __builtin_fmaf(fminf(q, 1e30f), 3.0f * C * 0.044715f, C), p);
     return a;
   } else if constexpr (ACT == kRelu2) {
     const float r = v < 0.0f ? 0.0f : v;  // NaN stays

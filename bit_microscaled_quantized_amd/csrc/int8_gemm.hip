@@ -69,8 +69,8 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_i
   }
   // The output leaves in whole rows of the wave's tile, through its share of the stages:
   // RB bytes of a token at a time, the 16-byte chunk c of token m in slot c ^ (m / (256 /
-  // RB)), which is free of bank conflicts both ways.  (Stored as the lanes hold it, 16 bytes of
-  // 32 tokens at a time, a tile's end took 8 us more.)
+  // RB)), which is free of bank conflicts both ways.  (Stored as the lanes hold it, 8 bytes of
+  // 32 tokens at a time, 8192 x 20480 x 5120 took 784 us, so 744.)
   constexpr int SIZE = sizeof(OutT), RB = WAVE * SIZE < 256 ? WAVE * SIZE : 256, CH = RB / 16;
   constexpr int PASSES = WAVE * SIZE / RB, IW = W / PASSES;
   __syncthreads();  // the stages are free
@@ -140,9 +140,15 @@ int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W
 
 constexpr int64_t slots_of(int W) { return W == 4 ? 256 : W == 2 ? 512 : 1024; }  // workgroups on 256 CUs
 
-// Time of a round of `tiles` (at most slots_of(W)) of so many stages, in microseconds.  A
-// stage takes longer the more of them run: of a CU's own (small tiles), of the caches and
-// of the chip's power.
+// Time of a round of `tiles` (at most slots_of(W)) of so many stages, in microseconds,
+// fitted to sweeps over W and parts.  A stage takes longer the more of them run: of a CU's
+// own (small tiles), of the caches and of the chip's power.  What W = 4, 2 and 1 take at
+// their best parts, in microseconds (M x N x K):
+//   8192 x 20480 x 5120   746, 856, -      4096 x 5120 x 20480   382, 424, 688
+//   1024 x  5120 x 20480  127, 154, 186    1024 x 20480 x 5120   133, 136, 193
+//    100 x  5120 x 20480   45,  40,  42     300 x  4096 x 4096    27,  21,  18
+// In one part the second pair takes 255 and 474 with W = 4: a tile over all of a long K while
+// most CUs idle.
 double round_us(int64_t tiles, double stages, int W) {
   const double full = (double)tiles / (double)slots_of(W);
   if (W == 4) return stages * (1.2 + 0.35 * full) + 10.0;
