@@ -9,9 +9,9 @@
 // Tiles that would leave most compute units idle in a round of their own (all of them, or
 // those behind the last full round) are split over K: the parts leave their integers in
 // the workspace, in the order of the lanes, and a second launch adds and scales them.
-#include "bf16_tile.hpp"
 #include "blocks_launch.hpp"
 #include "int8_device.hpp"
+#include "int8_ring.hpp"
 #include "per_device.hpp"
 
 namespace nvfp4 {
@@ -28,11 +28,18 @@ __device__ __forceinline__ void place(int t, int whole, int tiles, int num_n, in
   pm = id % width / rows;
 }
 
-// How a tile takes its stages: an even number of whole ones, any (SHIFT), or less than one.
-enum Stages { kEven, kAny, kOne };
+// How a tile takes its stages: an even number of whole ones, any (SHIFT), any in three
+// buffers (int8_ring.hpp), or less than one.
+enum Stages { kEven, kAny, kRing, kOne };
+
+constexpr int stages_lds(int W, int stages) { return stages == kRing ? ring_lds(W) : tile_lds(W); }
+// workgroups that share a compute unit, by its LDS (and, W = 4, its registers)
+constexpr int per_cu(int W, int stages) {
+  return W == 4 ? 1 : W == 2 ? (stages == kRing ? 1 : 2) : stages == kRing ? 3 : 4;
+}
 
 template <int W, int STAGES, typename OutT>
-__global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_int8_tile(GemmArgs g) {
+__global__ __launch_bounds__(TILE_THREADS, per_cu(W, STAGES)) void k_int8_tile(GemmArgs g) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int TILE = tile_side(W), WAVE = 32 * W;
   const int num_m = (g.M + TILE - 1) / TILE, num_n = (g.N + TILE - 1) / TILE, tiles = num_m * num_n;
@@ -51,7 +58,10 @@ __global__ __launch_bounds__(TILE_THREADS, W == 4 ? 1 : W == 2 ? 2 : 4) void k_i
   const TileOperand wt{reinterpret_cast<const uint16_t*>(g.b + (int64_t)n0 * g.ldb), (uint32_t)(g.ldb / 2), g.N - n0, 0};
   const TileOperand tok{reinterpret_cast<const uint16_t*>(g.a + (int64_t)m0 * g.lda), (uint32_t)(g.lda / 2), g.M - m0, 0};
   intx16 acc[W][W];
-  tile_product<W, false, false, STAGES != kOne, MfmaInt8, STAGES == kAny>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
+  if constexpr (STAGES == kRing)
+    ring_product<W>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
+  else
+    tile_product<W, false, false, STAGES != kOne, MfmaInt8, STAGES == kAny>(wt, tok, g.K / 2, kt0, kt1, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 5, lr = lane & 31;
   if (parts > 1) {
@@ -138,69 +148,70 @@ constexpr int64_t kFewTokens = 64;
 
 int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
 
-constexpr int64_t slots_of(int W) { return W == 4 ? 256 : W == 2 ? 512 : 1024; }  // workgroups on 256 CUs
+constexpr int64_t slots_of(int W, bool ring) { return 256 * per_cu(W, ring ? kRing : kAny); }  // workgroups on 256 CUs
 
-// Time of a round of `tiles` (at most slots_of(W)) of so many stages, in microseconds,
-// fitted to sweeps over W and parts.  A stage takes longer the more of them run: of a CU's
-// own (small tiles), of the caches and of the chip's power.  What W = 4, 2 and 1 take at
-// their best parts, in microseconds (M x N x K):
-//   8192 x 20480 x 5120   746, 856, -      4096 x 5120 x 20480   382, 424, 688
-//   1024 x  5120 x 20480  127, 154, 186    1024 x 20480 x 5120   133, 136, 193
-//    100 x  5120 x 20480   45,  40,  42     300 x  4096 x 4096    27,  21,  18
-// In one part the second pair takes 255 and 474 with W = 4: a tile over all of a long K while
-// most CUs idle.
-double round_us(int64_t tiles, double stages, int W) {
-  const double full = (double)tiles / (double)slots_of(W);
-  if (W == 4) return stages * (1.2 + 0.35 * full) + 10.0;
-  if (W == 2) return stages * (0.62 + 0.4 * full) + 6.0;
-  return stages * (0.4 + 0.6 * full) + 4.0;
+// Time of a round of `tiles` (at most slots_of) of so many stages, in microseconds, fitted
+// to sweeps over the four kinds of tile and their parts (39 shapes of 65 to 8192 tokens: what it
+// picks takes 0.9 % longer than the best of all in the mean, 10 % at most).  A stage takes
+// longer the more of them run: of a CU's own (small tiles), of the caches and of the
+// chip's power.  At their best parts W = 4, W = 2, W = 2 in three buffers and W = 1 take, in
+// microseconds (M x N x K; 8192 x 20480 x 5120 746, 856 and more):
+//   4096 x 5120 x 20480  376 416 490 656      1024 x 20480 x 5120  129 130 145 187
+//    100 x 5120 x 20480   46  38  33  41       300 x  4096 x  4096   27  20  19  13
+double round_us(int64_t tiles, double stages, int W, bool ring) {
+  const double full = (double)tiles / (double)slots_of(W, ring);
+  if (W == 4) return stages * (1.4 + 0.58 * full) + 8.4;
+  if (W == 2) return ring ? stages * (0.34 + 0.31 * full) + 4.7 : stages * (0.63 + 0.45 * full) + 6.1;
+  return stages * (0.22 + 0.55 * full) + 3.3;
 }
 
 struct Plan {
   int W, parts;
+  bool ring;
   int64_t tiles, whole, bytes;
 };
 double plan_us(const Plan& p, int64_t stages) {
-  const int64_t rest = p.tiles - p.whole, slots = slots_of(p.W);
-  double us = (double)(p.whole / slots) * round_us(slots, (double)stages, p.W);
-  if (p.whole % slots > 0) us += round_us(p.whole % slots, (double)stages, p.W);
+  const int64_t rest = p.tiles - p.whole, slots = slots_of(p.W, p.ring);
+  double us = (double)(p.whole / slots) * round_us(slots, (double)stages, p.W, p.ring);
+  if (p.whole % slots > 0) us += round_us(p.whole % slots, (double)stages, p.W, p.ring);
   if (rest > 0)  // and a launch that reads the parts' sums
-    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W) + 3.0 + (double)p.bytes * 2.0 / 6.0e6;
+    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W, p.ring) + 2.8 + (double)p.bytes * 2.0 / 6.0e6;
   return us;
 }
 // split false: whole tiles only
 Plan plan_of(int64_t M, int64_t N, int64_t K, bool split) {
   const int64_t stages = (K / 2 + TILE_K - 1) / TILE_K;
-  Plan best{0, 1, 0, 0, 0};
+  Plan best{0, 1, false, 0, 0, 0};
   double best_us = 0;
-  for (int W : {4, 2, 1}) {
+  for (const auto& [W, ring] : {std::pair{4, false}, {2, false}, {2, true}, {1, true}}) {
     if (K < 2 * TILE_K && W > 1) continue;
-    const int64_t tiles = tiles_of(M, W) * tiles_of(N, W), slots = slots_of(W);
+    const int64_t tiles = tiles_of(M, W) * tiles_of(N, W), slots = slots_of(W, ring);
     auto weigh = [&](const Plan& p) {
       const double us = plan_us(p, stages);
       if (best.W == 0 || us < best_us * 0.99) best = p, best_us = us;
     };
-    weigh(Plan{W, 1, tiles, tiles, 0});
+    weigh(Plan{W, 1, ring, tiles, tiles, 0});
     const int64_t whole = tiles / slots * slots, rest = tiles - whole;
     if (!split || rest == 0) continue;
     const int64_t most = std::min(slots / rest, stages / 4);
     for (int64_t parts = 2; parts <= most; parts++)
-      weigh(Plan{W, (int)parts, tiles, whole, parts * rest * tile_side(W) * tile_side(W) * 4});
+      weigh(Plan{W, (int)parts, ring, tiles, whole, parts * rest * tile_side(W) * tile_side(W) * 4});
   }
   return best;
 }
 
 template <int W, int STAGES, typename OutT>
 hipError_t tile_go(const GemmArgs& g, unsigned grid, hipStream_t s) {
-  if (tile_lds(W) > 64 * 1024) {
+  constexpr int LDS = stages_lds(W, STAGES);
+  if (LDS > 64 * 1024) {
     static std::atomic<uint64_t> done{0};
     const hipError_t e = once_per_device(done, [] {
       return hipFuncSetAttribute(reinterpret_cast<const void*>(&k_int8_tile<W, STAGES, OutT>),
-                                 hipFuncAttributeMaxDynamicSharedMemorySize, tile_lds(W));
+                                 hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
     });
     if (e != hipSuccess) return e;
   }
-  k_int8_tile<W, STAGES, OutT><<<grid, TILE_THREADS, tile_lds(W), s>>>(g);
+  k_int8_tile<W, STAGES, OutT><<<grid, TILE_THREADS, LDS, s>>>(g);
   return hipGetLastError();
 }
 
@@ -209,12 +220,14 @@ hipError_t gemm_w(const GemmArgs& g, const Plan& p, hipStream_t s) {
   const int64_t rest = p.tiles - p.whole;
   const unsigned grid = (unsigned)(p.whole + rest * p.parts);
   hipError_t e;
-  if (g.K % (4 * TILE_K) == 0 && rest == 0)
+  if constexpr (W == 1)
+    e = g.K >= 2 * TILE_K ? tile_go<1, kRing, OutT>(g, grid, s) : tile_go<1, kOne, OutT>(g, grid, s);
+  else if (W == 2 && p.ring)
+    e = tile_go<2, kRing, OutT>(g, grid, s);
+  else if (g.K % (4 * TILE_K) == 0 && rest == 0)
     e = tile_go<W, kEven, OutT>(g, grid, s);
-  else if (W > 1 || g.K >= 2 * TILE_K)
-    e = tile_go<W, kAny, OutT>(g, grid, s);
   else
-    e = tile_go<1, kOne, OutT>(g, grid, s);
+    e = tile_go<W, kAny, OutT>(g, grid, s);
   if (e != hipSuccess || rest == 0) return e;
   k_int8_join<W, OutT><<<(unsigned)(rest * W * W * 4), TILE_THREADS, 0, s>>>(g);
   return hipGetLastError();

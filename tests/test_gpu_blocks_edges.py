@@ -9,6 +9,22 @@ from bit_microscaled_quantized_amd import blocks
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("M,N,K", [
+    # tiles of 256 and of 128 behind full rounds, or all of them, in parts; K a multiple of two stages, and not
+    (4096, 5120, 20480), (4095, 5117, 20464), (512, 5120, 20480), (500, 5111, 20464),
+])
+def test_products_in_parts(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    a, b = (torch.randint(-127, 128, (r, K), generator=g, device="cuda", dtype=torch.int32).to(torch.int8) for r in (M, N))
+    sa, sb = (0.001 + torch.rand(r, generator=g, device="cuda") for r in (M, N))
+    assert nv.nvfp4_int8_gemm_workspace_size(M, N, K) > 0
+    want = ((a.double() @ b.double().t().contiguous()).float() * sb * sa[:, None]).to(torch.bfloat16)
+    assert torch.equal(blocks.int8_matmul(a, sa, b, sb), want)
+    c = torch.empty_like(want)
+    nv.nvfp4_int8_gemm(M, N, K, a, K, sa, b, K, sb, c, nv.NVFP4_BF16, N, None, 0)  # without a workspace
+    assert torch.equal(c, want)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu2"])
 def test_slopes_of_the_largest_activations(dtype, act):
