@@ -62,10 +62,42 @@ void with_act(int act, F&& f) {
   }
 }
 
-// A vector of a row (n of its elements inside it, n <= 0: none; the rest zero).
-template <typename T, bool STREAM>
-__device__ __forceinline__ u32x4_t load_or_zero(const T* p, int n) {
-  return n > 0 ? load_vec<T, STREAM>(p, n) : u32x4_t{0, 0, 0, 0};
+// A vector's elements from the sh-th on, zeros behind them.
+template <typename T>
+__device__ __forceinline__ void shift_down(u32x4_t& v, int sh) {
+  const int words = sizeof(T) == 4 ? sh : sh >> 1;
+  if (words & 4) v = u32x4_t{0, 0, 0, 0};
+  if (words & 2) v = u32x4_t{v[2], v[3], 0, 0};
+  if (words & 1) v = u32x4_t{v[1], v[2], v[3], 0};
+  if (sizeof(T) == 2 && (sh & 1))
+    v = u32x4_t{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+}
+
+// A row's vector from column c on (n of its elements inside it, n <= 0: none).  One that
+// ends past the row is read as the row's last whole one, for end_row to shift when all of a
+// lane's loads are under way (8192 x 5119 BF16 norms 91 us; with its elements read one after
+// the other 132).  WHOLE: none does.
+template <typename T, bool STREAM, bool WHOLE, typename I>
+__device__ __forceinline__ u32x4_t load_row(const T* row, I c, int n, uint32_t cols) {
+  constexpr int N = VecOf<T>::N;
+  if (n <= 0) return u32x4_t{0, 0, 0, 0};
+  if constexpr (WHOLE) return load_vec<T, STREAM>(row + c, N);
+  if (cols < (uint32_t)N) return VecOf<T>::load_n(row, n);
+  return load_vec<T, STREAM>(row + min(c, (I)(cols - N)), N);
+}
+// The rest of its elements zero.
+template <typename T>
+__device__ __forceinline__ void end_row(u32x4_t& v, int n, uint32_t cols) {
+  constexpr int N = VecOf<T>::N;
+  if (n > 0 && n < N && cols >= (uint32_t)N) shift_down<T>(v, N - n);
+}
+// Both
+template <typename T, bool STREAM, typename I>
+__device__ __forceinline__ u32x4_t load_or_zero(const T* row, I c, int n, uint32_t cols) {
+  u32x4_t v = load_row<T, STREAM, false>(row, c, n, cols);
+  end_row<T>(v, n, cols);
+  return v;
 }
 
 // The low bytes of four integers held as 1.5 * 2^23 + integer, in order.

@@ -98,9 +98,11 @@ __global__ __launch_bounds__(256) void k_act(ActArgs a) {
   const uint32_t item = blockIdx.x * 256 + threadIdx.x;
   const uint32_t row = divide(item, a.per_row), c = (item - row * a.per_row.d) * N;
   const int n = item < a.items && c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
-  const u32x4_t g = load_or_zero<T, STREAM>(static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g + c, n);
-  const u32x4_t u = load_or_zero<T, STREAM>(static_cast<const T*>(a.up) + (int64_t)row * a.ld_u + c,
-                                            a.up == nullptr ? 0 : n);
+  u32x4_t g = load_row<T, STREAM, false>(static_cast<const T*>(a.gate) + (int64_t)row * a.ld_g, c, n, a.cols);
+  u32x4_t u = load_row<T, STREAM, false>(static_cast<const T*>(a.up) + (int64_t)row * a.ld_u, c, a.up == nullptr ? 0 : n,
+                                  a.cols);
+  end_row<T>(g, n, a.cols);
+  end_row<T>(u, n, a.cols);
   float fg[N], fu[N];
   VecOf<T>::unpack(g, fg);
   VecOf<T>::unpack(u, fu);
@@ -138,14 +140,19 @@ struct Kept {
   uint32_t scale;
   __device__ __forceinline__ void load(const int8_t* codes, const uint8_t* scales, uint32_t row, uint32_t c, int n,
                                        uint32_t cols, uint32_t blocks) {
-    const int8_t* p = codes + (int64_t)row * cols + c;
-    if (n >= N) {
+    const int8_t* p = codes + (int64_t)row * cols;
+    if (cols >= (uint32_t)N) {  // past the row's end: its last whole vector, shifted
+      p += min(c, cols - N);
+      uint64_t v;
       if constexpr (N == 8) {
-        const u32x2_t v = *reinterpret_cast<const u32x2_a1*>(p);
-        w[0] = v[0], w[1] = v[1];
+        const u32x2_t u = *reinterpret_cast<const u32x2_a1*>(p);
+        v = (uint64_t)u[1] << 32 | u[0];
       } else {
-        w[0] = *reinterpret_cast<const u32_a1*>(p);
+        v = *reinterpret_cast<const u32_a1*>(p);
       }
+      v >>= 8 * (N - n);
+      w[0] = (uint32_t)v;
+      if constexpr (N == 8) w[1] = (uint32_t)(v >> 32);
     } else {
 #pragma unroll
       for (int u = 0; u < N / 4; u++) w[u] = 0;
@@ -177,8 +184,8 @@ __global__ __launch_bounds__(256) void k_act_back(ActBackArgs a) {
   Kept<N> kg, ku;
   kg.load(a.gate_codes, a.gate_scales, row, c, n, a.cols, a.blocks);
   if (a.up_codes != nullptr) ku.load(a.up_codes, a.up_scales, row, c, n, a.cols, a.blocks);
-  const u32x4_t d = load_or_zero<T, STREAM>(static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy + c,
-                                            a.dy == nullptr ? 0 : n);
+  const u32x4_t d = load_or_zero<T, STREAM>(static_cast<const T*>(a.dy) + (int64_t)row * a.ld_dy, c,
+                                            a.dy == nullptr ? 0 : n, a.cols);
   float g[N], u[N], dy[N], slope[N];
   kg.values(g);
   VecOf<T>::unpack(d, dy);

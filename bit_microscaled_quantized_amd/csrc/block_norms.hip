@@ -6,7 +6,7 @@
 // j + G, ..., up to VPT of them, which stay in registers over both of the row's sums
 // (and, with codes as output, its maximum); rows wider than a workgroup's registers
 // are read once per sum and once more.  Sums are FP32 in a fixed order.
-// 8192 x 5120 BF16 with a gate per row: 420 MB in 72 us (5.8 TB/s; a copy of tensors of that
+// 8192 x 5120 BF16 with a gate per row: 420 MB in 69 us (6.1 TB/s; a copy of tensors of that
 // size reaches 6.2), backward 671 MB in 122 us (5.5 TB/s, with the sums over rows).
 #include "act_device.hpp"
 #include "blocks_launch.hpp"
@@ -56,15 +56,31 @@ __device__ __forceinline__ T* at_row(P* p, uint32_t row, int64_t ld, uint32_t of
     return reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(start) + off);
 }
 
+// N gains from column c on, n (more than 0) of them inside the row; zeros behind them.
+template <int N, bool WHOLE, typename I>
+__device__ __forceinline__ void load_gains(const void* gamma, int f32, I c, int n, uint32_t cols, float* g) {
+  if constexpr (WHOLE) {
+    load_gamma<N>(gamma, f32, (uint32_t)c, N, g);
+  } else if (f32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      VecOf<float>::unpack(load_or_zero<float, false>(static_cast<const float*>(gamma), c + i, n - i, cols), g + i);
+  } else if constexpr (N == 8) {
+    VecOf<uint16_t>::unpack(load_or_zero<uint16_t, false>(static_cast<const uint16_t*>(gamma), c, n, cols), g);
+  } else {
+    load_gamma<N>(gamma, 0, (uint32_t)c, n, g);
+  }
+}
+
 // f becomes h: residual + scale * (g * ((x * rstd) * gamma)); elements past the row's end stay 0
-template <typename T>
+template <typename T, bool WHOLE = false>
 __device__ __forceinline__ void sum_vec(const NormsArgs& a, float* f, u32x4_t r, u32x4_t gate, float rstd, uint32_t c,
                                         int n) {
   constexpr int N = VecOf<T>::N;
   float gm[N], fr[N], fg[N];
 #pragma unroll
   for (int i = 0; i < N; i++) gm[i] = 0.0f;
-  if (n > 0) load_gamma<N>(a.post, a.gamma_f32, c, n, gm);
+  if (n > 0) load_gains<N, WHOLE>(a.post, a.gamma_f32, c, n, a.cols, gm);
   VecOf<T>::unpack(r, fr);
 #pragma unroll
   for (int i = 0; i < N; i++) f[i] = (f[i] * rstd) * gm[i];
@@ -78,18 +94,20 @@ __device__ __forceinline__ void sum_vec(const NormsArgs& a, float* f, u32x4_t r,
 }
 
 // f becomes y: (h * rstd) * gamma, zeros past the row's end
-template <typename T>
+template <typename T, bool WHOLE = false>
 __device__ __forceinline__ void norm_vec(const NormsArgs& a, float* f, float rstd, uint32_t c, int n) {
   constexpr int N = VecOf<T>::N;
   float gm[N];
 #pragma unroll
   for (int i = 0; i < N; i++) gm[i] = 0.0f;
-  if (n > 0) load_gamma<N>(a.pre, a.gamma_f32, c, n, gm);
+  if (n > 0) load_gains<N, WHOLE>(a.pre, a.gamma_f32, c, n, a.cols, gm);
 #pragma unroll
   for (int i = 0; i < N; i++) f[i] = i < n ? (f[i] * rstd) * gm[i] : 0.0f;
 }
 
-template <typename T, int VPT, bool CODES, bool STREAM>
+// WHOLE: rows are whole vectors (32768 x 1024 BF16 57 us, 61 with what an end inside one
+// takes).
+template <typename T, int VPT, bool CODES, bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(1024) void k_block_norms(NormsArgs a, int G) {
   constexpr int N = VecOf<T>::N;
   __shared__ float red[16];
@@ -98,18 +116,26 @@ __global__ __launch_bounds__(1024) void k_block_norms(NormsArgs a, int G) {
   const T* xr = static_cast<const T*>(a.x) + (int64_t)row * a.ld_x;
   const T* rr = static_cast<const T*>(a.residual) + (int64_t)row * a.ld_r;
   const T* gr = static_cast<const T*>(a.gate) + (int64_t)row * a.ld_gate;
+  // a vector's elements inside the row, from column c on
+  auto part = [&](uint32_t c) { return !live ? 0 : WHOLE ? (c < a.cols ? N : 0) : inside<N>(c, a.cols); };
   u32x4_t vx[VPT], vr[VPT], vg[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const uint32_t c = (j + k * G) * N;
-    const int n = live ? inside<N>(c, a.cols) : 0;
-    vx[k] = load_or_zero<T, STREAM>(xr + c, n);
-    vr[k] = load_or_zero<T, STREAM>(rr + c, a.residual == nullptr ? 0 : n);
-    vg[k] = load_or_zero<T, false>(gr + c, a.gate == nullptr ? 0 : n);
+    const int n = part(c);
+    vx[k] = load_row<T, STREAM, WHOLE>(xr, c, n, a.cols);
+    vr[k] = load_row<T, STREAM, WHOLE>(rr, c, a.residual == nullptr ? 0 : n, a.cols);
+    vg[k] = load_row<T, false, WHOLE>(gr, c, a.gate == nullptr ? 0 : n, a.cols);
   }
   float f[VPT][N], sq = 0.0f;
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
+    if constexpr (!WHOLE) {
+      const int n = part((j + k * G) * N);
+      end_row<T>(vx[k], n, a.cols);
+      end_row<T>(vr[k], n, a.cols);
+      end_row<T>(vg[k], n, a.cols);
+    }
     VecOf<T>::unpack(vx[k], f[k]);
 #pragma unroll
     for (int i = 0; i < N; i++) sq = __builtin_fmaf(f[k][i], f[k][i], sq);
@@ -119,10 +145,10 @@ __global__ __launch_bounds__(1024) void k_block_norms(NormsArgs a, int G) {
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const uint32_t c = (j + k * G) * N;
-    const int n = live ? inside<N>(c, a.cols) : 0;
-    sum_vec<T>(a, f[k], vr[k], vg[k], post, c, n);
+    const int n = part(c);
+    sum_vec<T, WHOLE>(a, f[k], vr[k], vg[k], post, c, n);
     if (n > 0 && a.h != nullptr)
-      store_vec<T, STREAM>(static_cast<T*>(a.h) + (int64_t)row * a.ld_h + c, VecOf<T>::pack(f[k]), n);
+      store_vec<T, STREAM>(static_cast<T*>(a.h) + (int64_t)row * a.ld_h + c, VecOf<T>::pack(f[k]), WHOLE ? N : n);
 #pragma unroll
     for (int i = 0; i < N; i++) sq = __builtin_fmaf(f[k][i], f[k][i], sq);
   }
@@ -135,12 +161,12 @@ __global__ __launch_bounds__(1024) void k_block_norms(NormsArgs a, int G) {
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
     const uint32_t c = (j + k * G) * N;
-    const int n = live ? inside<N>(c, a.cols) : 0;
-    norm_vec<T>(a, f[k], pre, c, n);
+    const int n = part(c);
+    norm_vec<T, WHOLE>(a, f[k], pre, c, n);
     if constexpr (CODES)
       m = most_of<N>(f[k], m);
     else if (n > 0)
-      store_vec<T, STREAM>(static_cast<T*>(a.y) + (int64_t)row * a.ld_y + c, VecOf<T>::pack(f[k]), n);
+      store_vec<T, STREAM>(static_cast<T*>(a.y) + (int64_t)row * a.ld_y + c, VecOf<T>::pack(f[k]), WHOLE ? N : n);
   }
   if constexpr (CODES) {
     const RowCode q(group_max(m, G, reinterpret_cast<uint32_t*>(red)));
@@ -173,14 +199,14 @@ __global__ __launch_bounds__(1024) void k_block_norms_wide(NormsArgs a) {
   float sq = 0.0f;
   for (uint64_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {
     float f[N];
-    VecOf<T>::unpack(load_vec(xr + c, inside<N>(c, a.cols)), f);
+    VecOf<T>::unpack(load_or_zero<T, false>(xr, c, inside<N>(c, a.cols), a.cols), f);
     sq += sum_of(f);
   }
   const float post = rstd_of(group_sum(sq, 1024, red), a.cols, a.eps);
   auto h_of = [&](uint64_t c, int n, float* f) {
-    VecOf<T>::unpack(load_or_zero<T, false>(xr + c, n), f);
-    sum_vec<T>(a, f, load_or_zero<T, false>(rr + c, a.residual == nullptr ? 0 : n),
-               load_or_zero<T, false>(gr + c, a.gate == nullptr ? 0 : n), post, (uint32_t)c, n);
+    VecOf<T>::unpack(load_or_zero<T, false>(xr, c, n, a.cols), f);
+    sum_vec<T>(a, f, load_or_zero<T, false>(rr, c, a.residual == nullptr ? 0 : n, a.cols),
+               load_or_zero<T, false>(gr, c, a.gate == nullptr ? 0 : n, a.cols), post, (uint32_t)c, n);
   };
   sq = 0.0f;
   for (uint64_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {
@@ -324,18 +350,6 @@ __device__ __forceinline__ void pack_four(u32x4_t& v, int u, const float* f) {
     v[2 * u] = bf16_pack(f[0], f[1]);
     v[2 * u + 1] = bf16_pack(f[2], f[3]);
   }
-}
-
-// A vector's elements from the sh-th on, zeros behind them.
-template <typename T>
-__device__ __forceinline__ void shift_down(u32x4_t& v, int sh) {
-  const int words = sizeof(T) == 4 ? sh : sh >> 1;
-  if (words & 4) v = u32x4_t{0, 0, 0, 0};
-  if (words & 2) v = u32x4_t{v[2], v[3], 0, 0};
-  if (words & 1) v = u32x4_t{v[1], v[2], v[3], 0};
-  if (sizeof(T) == 2 && (sh & 1))
-    v = u32x4_t{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
-                __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
 }
 
 // Another offset for all that the compiler knows: sums of it with the bases of the
@@ -758,10 +772,11 @@ hipError_t norms_t(const NormsArgs& a, hipStream_t s) {
   const bool stream = (int64_t)a.rows * a.cols * 4 * (int64_t)sizeof(T) >= kStreamBytes;
   with_vpt(r.vpt, [&](auto vpt) {
     constexpr int VPT = vpt.value <= 5 ? vpt.value : 1;
-    if (stream)
-      k_block_norms<T, VPT, CODES, true><<<grid, threads, 0, s>>>(a, r.G);
-    else
-      k_block_norms<T, VPT, CODES, false><<<grid, threads, 0, s>>>(a, r.G);
+    auto* kernel = a.cols % N == 0
+                       ? stream ? &k_block_norms<T, VPT, CODES, true, true> : &k_block_norms<T, VPT, CODES, false, true>
+                   : stream ? &k_block_norms<T, VPT, CODES, true, false>
+                            : &k_block_norms<T, VPT, CODES, false, false>;
+    kernel<<<grid, threads, 0, s>>>(a, r.G);
   });
   return hipGetLastError();
 }

@@ -49,13 +49,17 @@ __global__ __launch_bounds__(1024) void k_int8_rows(QuantArgs a, int G) {
   for (int k = 0; k < VPT; k++) {
     const uint32_t c = (j + k * G) * N;
     const int n = live && c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
-    g[k] = load_or_zero<T, STREAM>(gr + c, n);
-    u[k] = load_or_zero<T, STREAM>(ur + c, a.up == nullptr ? 0 : n);
+    g[k] = load_row<T, STREAM, false>(gr, c, n, a.cols);
+    u[k] = load_row<T, STREAM, false>(ur, c, a.up == nullptr ? 0 : n, a.cols);
   }
   float f[VPT][N];
   uint32_t m = 0;
 #pragma unroll
   for (int k = 0; k < VPT; k++) {
+    const uint32_t c = (j + k * G) * N;
+    const int n = live && c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
+    end_row<T>(g[k], n, a.cols);
+    end_row<T>(u[k], n, a.cols);
     values_of<T, ACT>(a, g[k], u[k], f[k]);  // zeros past the row's end
     m = most_of<N>(f[k], m);
   }
@@ -80,7 +84,8 @@ __global__ __launch_bounds__(1024) void k_int8_wide(QuantArgs a) {
   const T* ur = static_cast<const T*>(a.up) + (int64_t)row * a.ld_u;
   auto at = [&](uint32_t c, float* f) {
     const int n = c < a.cols ? (int)min(a.cols - c, (uint32_t)N) : 0;
-    values_of<T, ACT>(a, load_or_zero<T, false>(gr + c, n), load_or_zero<T, false>(ur + c, a.up == nullptr ? 0 : n), f);
+    values_of<T, ACT>(a, load_or_zero<T, false>(gr, c, n, a.cols),
+                      load_or_zero<T, false>(ur, c, a.up == nullptr ? 0 : n, a.cols), f);
   };
   uint32_t m = 0;
   for (uint32_t c = threadIdx.x * N; c < a.cols; c += 1024 * N) {  // fewer than 2^31 columns
