@@ -155,18 +155,19 @@ int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W
 constexpr int64_t slots_of(int W, bool ring) { return 256 * per_cu(W, ring ? kRing : kAny); }  // workgroups on 256 CUs
 
 // Time of a round of `tiles` (at most slots_of) of so many stages, in microseconds, fitted
-// to sweeps over the four kinds of tile and their parts (39 shapes of 65 to 8192 tokens: what it
-// picks takes 0.9 % longer than the best of all in the mean, 10 % at most).  A stage takes
+// to sweeps over the four kinds of tile and their parts (55 shapes of 65 to 16384 tokens: what it
+// picks takes 0.5 % longer than the best of all in the mean, 6 % at most).  A stage takes
 // longer the more of them run: of a CU's own (small tiles), of the caches and of the
 // chip's power.  At their best parts W = 4, W = 2, W = 2 in three buffers and W = 1 take, in
 // microseconds (M x N x K; 8192 x 20480 x 5120 746, 856 and more):
 //   4096 x 5120 x 20480  376 416 490 656      1024 x 20480 x 5120  129 130 145 187
 //    100 x 5120 x 20480   46  38  33  41       300 x  4096 x  4096   27  20  19  13
+//   6061 x 11072 x   512   93  72 115 103
 double round_us(int64_t tiles, double stages, int W, bool ring) {
   const double full = (double)tiles / (double)slots_of(W, ring);
-  if (W == 4) return stages * (1.4 + 0.58 * full) + 8.4;
-  if (W == 2) return ring ? stages * (0.34 + 0.31 * full) + 4.7 : stages * (0.63 + 0.45 * full) + 6.1;
-  return stages * (0.22 + 0.55 * full) + 3.3;
+  if (W == 4) return stages * (1.22 + 0.41 * full) + 13.5;
+  if (W == 2) return ring ? stages * (0.35 + 0.28 * full) + 4.6 : stages * (0.6 + 0.46 * full) + 4.7;
+  return stages * (0.22 + 0.54 * full) + 3.3;
 }
 
 struct Plan {
@@ -179,7 +180,7 @@ double plan_us(const Plan& p, int64_t stages) {
   double us = (double)(p.whole / slots) * round_us(slots, (double)stages, p.W, p.ring);
   if (p.whole % slots > 0) us += round_us(p.whole % slots, (double)stages, p.W, p.ring);
   if (rest > 0)  // and a launch that reads the parts' sums
-    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W, p.ring) + 2.8 + (double)p.bytes * 2.0 / 6.0e6;
+    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W, p.ring) + 3.1 + (double)p.bytes * 2.0 / 6.0e6;
   return us;
 }
 // split false: whole tiles only

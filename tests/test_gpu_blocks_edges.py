@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("M,N,K", [
     # tiles of 256 and of 128 behind full rounds, or all of them, in parts; K a multiple of two stages, and not
-    (4096, 5120, 20480), (4095, 5117, 20464), (512, 5120, 20480), (500, 5111, 20464),
+    (4096, 5120, 20480), (4095, 5117, 20464), (512, 5120, 20480), (500, 5111, 20464), (100, 5111, 20464),
 ])
 def test_products_in_parts(M, N, K):
     g = torch.Generator(device="cuda").manual_seed(M + K)
