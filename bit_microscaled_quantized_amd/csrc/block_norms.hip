@@ -759,10 +759,11 @@ template <typename T, bool CODES>
 hipError_t norms_t(const NormsArgs& a, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
   const int64_t vecs = ((CODES ? (int64_t)a.padded : (int64_t)a.cols) + N - 1) / N;
-  // Two vectors a lane and half the waves where rows are many (8192 x 5120 BF16 72 us, 85 with
-  // one, 74 with three), one where a launch is as long as its longest row (48 x 5120 4.4 us, 5.1
-  // with two); rows of up to 128 vectors are level.
-  const RowShape r = row_shape(vecs, a.rows >= 1024 && vecs > 128 ? 2 : 1);
+  // Two vectors a lane and half the waves where rows are many (BF16 with a gate per row: 8192 x
+  // 5120 68 us, 79 with one, 68 with three; 32768 x 1024 54, 59, 55; 32768 x 256 19 and 21).  One where
+  // a launch is as long as its longest row (48 x 5120 4.5 us, 4.7 with two), and up to the 16 vectors
+  // that a group has lanes for (32768 x 128 12.0, 13.2 with two).
+  const RowShape r = row_shape(vecs, a.rows >= 512 && vecs > 16 ? 2 : 1);
   if (r.vpt == 0 || r.vpt > 5) {
     k_block_norms_wide<T, CODES><<<a.rows, 1024, 0, s>>>(a);
     return hipGetLastError();
