@@ -280,21 +280,26 @@ def _no_grad(*tensors):
         raise RuntimeError("the 8-bit product has no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
+def _code_rows(rows, K, device):
+    """Rows of K codes, each starting on a line of 128 bytes: the product reads those whole (1 x 20480 x 5136 19.0 us,
+    25.0 with rows next to each other; 8192 x 5120 x 5136 232 and 265)."""
+    return torch.empty((rows, (K + 127) // 128 * 128), dtype=torch.int8, device=device)[:, :K]
+
+
 def _code_buffers(rows, cols, device):
-    return (torch.empty((rows, _pad16(cols)), dtype=torch.int8, device=device),
-            torch.empty(rows, dtype=torch.float32, device=device))
+    return _code_rows(rows, _pad16(cols), device), torch.empty(rows, dtype=torch.float32, device=device)
 
 
 def int8_quantize(x):
-    """(codes, scales) of x's rows: int8 codes [rows, columns up to a multiple of 16] (zeros past the last column), one
-    FP32 scale per row."""
+    """(codes, scales) of x's rows: int8 codes [rows, columns up to a multiple of 16] (zeros past the last column; rows
+    start on 128-byte lines), one FP32 scale per row."""
     _no_grad(x)
     _on_gpu(x)
     _columns(x)
     m, ld = _rows(x)
     rows, cols = m.shape
     codes, scales = _code_buffers(rows, cols, x.device)
-    nv.nvfp4_int8_quantize(m, _dt(m), rows, cols, ld, codes, codes.shape[1], scales)
+    nv.nvfp4_int8_quantize(m, _dt(m), rows, cols, ld, codes, codes.stride(0), scales)
     return codes, scales
 
 
@@ -309,7 +314,7 @@ def int8_quantize_gated(gate, up=None, act: str = "silu"):
     u, ld_u = _opt_rows(up)
     rows, cols = g.shape
     codes, scales = _code_buffers(rows, cols, gate.device)
-    nv.nvfp4_int8_quantize_gated(act, g, u, _dt(g), rows, cols, ld_g, ld_u, codes, codes.shape[1], scales)
+    nv.nvfp4_int8_quantize_gated(act, g, u, _dt(g), rows, cols, ld_g, ld_u, codes, codes.stride(0), scales)
     return codes, scales
 
 
@@ -322,7 +327,7 @@ def block_norms_int8(x, residual, post_gamma, pre_gamma, gate=None, scale: float
     h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     codes, scales = _code_buffers(rows, cols, x.device)
     nv.nvfp4_block_norms(m, r, g, _dt(m), rows, cols, ld, ld_r, ld_g, int(bool(sigmoid)), post, pre, _dt(post), float(eps),
-                         float(scale), h, cols, None, 0, codes, codes.shape[1], scales, None, None)
+                         float(scale), h, cols, None, 0, codes, codes.stride(0), scales, None, None)
     return h, codes, scales
 
 
@@ -380,6 +385,8 @@ class Int8Linear(torch.nn.Module):
         super()._apply(fn, recurse)
         if self.scales.dtype != torch.float32:  # a change of the model's type leaves the scales in FP32
             self.scales = scales.to(self.scales.device)
+        if self.codes.stride(0) % 128 != 0:  # a copy has packed the rows
+            self.codes = _code_rows(*self.codes.shape, self.codes.device).copy_(self.codes)
         return self
 
     def _inputs(self, x):

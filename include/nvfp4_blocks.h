@@ -68,7 +68,8 @@ nvfp4_status nvfp4_int8_quantize_gated(int act, const void *gate, const void *up
  *   with the sum exact (32-bit integers), rounded to FP32 and multiplied by the
  *   scales in this order in FP32; c of type c_dt.
  *   a [M][lda], b [N][ldb] int8 codes (any value), 16-byte aligned, ld multiples of
- *   16 below 2^23; a_scales [M], b_scales [N] FP32; c [M][ldc].  M >= 0, N >= 1,
+ *   16 below 2^23 (rows that start on 128-byte lines are read in whole ones, up to a
+ *   third sooner); a_scales [M], b_scales [N] FP32; c [M][ldc].  M >= 0, N >= 1,
  *   both < 2^24, M * N <= 2^35; K a multiple of 16 in [16, 131056] (beyond which the sum
  *   could overflow).
  *   workspace: nvfp4_int8_gemm_workspace_size(M, N, K) bytes, 16-byte aligned, in

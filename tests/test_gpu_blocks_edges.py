@@ -131,3 +131,23 @@ def test_a_backward_pass_in_a_graph():
         torch.cuda.synchronize()
         for got, want in zip(out, grads()):
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 7])
+def test_rows_of_codes_start_on_lines(rows):
+    """The codes' buffer is wider than the codes; a module's moves, copies and states keep its results."""
+    torch.manual_seed(3)
+    x = torch.randn(rows, 88, device="cuda", dtype=torch.bfloat16)
+    codes, scales = blocks.int8_quantize(x)
+    assert codes.shape == (rows, 96) and codes.stride() == (128, 1) and codes.data_ptr() % 128 == 0
+    assert not codes[:, 88:].any()
+    layer = blocks.Int8Linear(torch.randn(40, 88, device="cuda"))
+    want = layer(x)
+    exact = (codes.double() @ layer.codes.double().t().contiguous()).float() * layer.scales * scales[:, None]
+    assert torch.equal(want, exact.to(torch.bfloat16))
+    there = layer.cpu().cuda()
+    assert there.codes.stride(0) == 128 and torch.equal(there(x), want)
+    other = blocks.Int8Linear(torch.randn(40, 88, device="cuda"))
+    other.load_state_dict(layer.state_dict())
+    assert other.codes.stride(0) == 128 and torch.equal(other(x), want)
+    assert torch.equal(blocks.int8_matmul(codes.contiguous(), scales, layer.codes.contiguous(), layer.scales, torch.bfloat16), want)
