@@ -13,7 +13,8 @@ inputs are kept in 8 bits, and the product of 8-bit integers for serving.
 Formulas, roundings and formats are those of include/nvfp4_blocks.h.  BF16 and FP32
 tensors, any leading dimensions; rows may be slices of a wider buffer.  Everything runs
 on torch's current stream, on the current device, with buffers from its caching
-allocator.
+allocator.  A backward pass is captured into a graph through torch.autograd.grad, or while
+no eager graph of the same leaves lives.
 """
 from __future__ import annotations
 
