@@ -1,4 +1,4 @@
-// The product of 8-bit integers for a few tokens (nvfp4_int8_gemm up to 64), gfx950:
+// The product of 8-bit integers for a few tokens (nvfp4_int8_gemm; up to 64), gfx950:
 // bound by reading the weight, which streams from HBM past the tokens' codes.
 //
 // A wave takes 16 weight rows in stages of 256 values of k.  It loads them in whole

@@ -147,15 +147,17 @@ __global__ __launch_bounds__(TILE_THREADS) void k_int8_join(GemmArgs g) {
   store_four<OutT>(g, m, n, v, bs, g.a_scales[m]);
 }
 
-// Up to here the weight streams past the tokens.
-constexpr int64_t kFewTokens = 64;
+// The weight streams past the tokens: up to 16, and up to 64 where it is so large that its
+// bytes are the time (48 x 5120 x 20480 26.6 us, 28.9 in tiles; 64 x 4096 x 4096 12.7, 10.1 in
+// tiles; 48 x 8192 x 4096 14.1 and 15.5; 24 x 4096 x 4096 9.9 and 8.7).
+bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K >= (int64_t(1) << 25)); }
 
 int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
 
 constexpr int64_t slots_of(int W, bool ring) { return 256 * per_cu(W, ring ? kRing : kAny); }  // workgroups on 256 CUs
 
 // Time of a round of `tiles` (at most slots_of) of so many stages, in microseconds, fitted
-// to sweeps over the four kinds of tile and their parts (55 shapes of 65 to 16384 tokens: what it
+// to sweeps over the four kinds of tile and their parts (60 shapes of 64 to 16384 tokens: what it
 // picks takes 0.5 % longer than the best of all in the mean, 6 % at most).  A stage takes
 // longer the more of them run: of a CU's own (small tiles), of the caches and of the
 // chip's power.  At their best parts W = 4, W = 2, W = 2 in three buffers and W = 1 take, in
@@ -179,8 +181,9 @@ double plan_us(const Plan& p, int64_t stages) {
   const int64_t rest = p.tiles - p.whole, slots = slots_of(p.W, p.ring);
   double us = (double)(p.whole / slots) * round_us(slots, (double)stages, p.W, p.ring);
   if (p.whole % slots > 0) us += round_us(p.whole % slots, (double)stages, p.W, p.ring);
-  if (rest > 0)  // and a launch that reads the parts' sums
-    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W, p.ring) + 3.1 + (double)p.bytes * 2.0 / 6.0e6;
+  if (rest > 0)  // and a launch that reads the parts' sums, one after the other
+    us += round_us(rest * p.parts, (double)((stages + p.parts - 1) / p.parts), p.W, p.ring) + 2.8 + 0.1 * p.parts +
+          (double)p.bytes * 2.0 / 6.0e6;
   return us;
 }
 // split false: whole tiles only
@@ -248,13 +251,13 @@ hipError_t gemm_t(const GemmArgs& g, const Plan& p, hipStream_t s) {
 }  // namespace
 
 int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
-  return M == 0 ? 0 : M <= kFewTokens ? few_plan(M, N, K).bytes : plan_of(M, N, K, true).bytes;
+  return M == 0 ? 0 : few_tokens(M, N, K) ? few_plan(M, N, K).bytes : plan_of(M, N, K, true).bytes;
 }
 
 hipError_t launch_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* a_scales,
                             const int8_t* b, int64_t ldb, const float* b_scales, void* c, int c_dt, int64_t ldc,
                             void* workspace, int64_t workspace_bytes, hipStream_t s) {
-  if (M <= kFewTokens) {
+  if (few_tokens(M, N, K)) {
     const FewPlan f = few_plan(M, N, K);
     const bool split = f.parts > 1 && workspace != nullptr && workspace_bytes >= f.bytes;
     const GemmArgs g{a,   b,   a_scales, b_scales, c, split ? static_cast<int*>(workspace) : nullptr,

@@ -56,6 +56,21 @@ def test_scales_that_need_a_gradient_are_refused():
         blocks.int8_matmul(codes, scales.requires_grad_(), codes, scales.detach())
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (17, 33000, 1040), (33, 4100, 8208), (49, 70000, 496), (32, 2300, 20464), (60, 1700, 20464), (64, 512, 131056),
+    (33, 3000, 11200), (17, 2 ** 21, 16), (50, 8191, 4112), (16, 8000, 4112)])
+def test_large_weights_stream_past_shared_tokens(M, N, K):
+    """Weights of 2^25 codes and more, whole and in parts, K that ends inside a stage, N inside a group of rows."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    a, b = (torch.empty(r, K, device="cuda", dtype=torch.int8).random_(-127, 128, generator=g) for r in (M, N))
+    sa, sb = (0.001 + torch.rand(r, generator=g, device="cuda") for r in (M, N))
+    want = (a.double() @ b.double().t().contiguous()).float() * sb * sa[:, None]
+    assert torch.equal(blocks.int8_matmul(a, sa, b, sb, torch.float32), want)
+    c = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+    nv.nvfp4_int8_gemm(M, N, K, a, K, sa, b, K, sb, c, nv.NVFP4_BF16, N, None, 0)  # without a workspace
+    assert torch.equal(c, want.to(torch.bfloat16))
+
+
 def test_two_graphs_share_a_workspace():
     """Calls in two captured graphs with one workspace, replayed in turn on one stream, with
     eager work between: the same results as alone."""

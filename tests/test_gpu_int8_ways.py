@@ -23,8 +23,8 @@ def product(torch, a, sa, b, sb):
     (1, 12000, 512, False), (3, 10240, 5120, False), (8, 20000, 272, False), (1, 100, 20480, True), (7, 1000, 40976, True),
     (16, 1024, 5120, False), (12, 333, 20464, True), (2, 40, 131056, True), (1, 65, 304, False), (5, 16385, 1040, False),
     # shared by four waves, whole and in parts, every number of tiles of tokens
-    (16, 10000, 4096, True), (11, 41000, 1040, False), (17, 300, 512, False), (32, 5120, 2064, True), (33, 70, 9008, True),
-    (48, 41100, 1024, False), (49, 1000, 784, True), (64, 5120, 20480, True), (64, 64, 131056, True), (50, 130, 16, False),
+    (16, 10000, 4096, True), (11, 41000, 1040, False), (17, 300, 512, False), (32, 5120, 2064, False), (33, 70, 9008, True),
+    (48, 41100, 1024, False), (49, 1000, 784, False), (64, 5120, 20480, True), (64, 64, 131056, True), (50, 130, 16, False),
     # 64 x 64 tiles: less than a stage, whole stages, any, in parts
     (65, 100, 16, False), (300, 257, 112, False), (100, 2048, 512, False), (257, 4999, 2048, False), (130, 1000, 400, False),
     (128, 1024, 5120, True), (70, 300, 20000, True), (66, 65, 128, False), (100, 100, 256, False), (90, 200, 144, False),
