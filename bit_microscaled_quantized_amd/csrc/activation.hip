@@ -65,7 +65,8 @@ __device__ __forceinline__ void keep(const float* f, uint32_t row, uint32_t c, i
   if (n <= 0) return;
   // m = a * 2^E, 1 <= a < 2: 127 = 1.984375 * 2^6, so the exponent is E - 6 for a <=
   // 1.984375 and E - 5 above.  A subnormal's E reads as -127, its limit for -133 is
-  // 127 * 2^-133 = 0x7F0000 * 2^-149.
+  // 127 * 2^-133 = 0x7F0000 * 2^-149.  Under the largest exponent, 121, codes saturate on both
+  // sides (-128 * 2^121 would be an infinity).
   const bool finite = m < 0x7F800000u;
   int e = (int)(m >> 23) - 127 - 6 + ((m & 0x7FFFFFu) > (m < 0x800000u ? 0x7F0000u : 0x7E0000u) ? 1 : 0);
   e = min(e, 121);
@@ -74,7 +75,8 @@ __device__ __forceinline__ void keep(const float* f, uint32_t row, uint32_t c, i
   for (int u = 0; u < N / 4; u++) {
     float t[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) t[i] = fminf(__builtin_amdgcn_ldexpf(f[4 * u + i], -e), 127.0f) + kToInt;
+    for (int i = 0; i < 4; i++)
+      t[i] = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(f[4 * u + i], -e), -127.0f, 127.0f) + kToInt;
     w[u] = finite ? bytes_of(t[0], t[1], t[2], t[3]) : 0u;
   }
   int8_t* p = codes + (int64_t)row * cols + c;

@@ -27,8 +27,9 @@
  * shorter) share one UE8M0 scale byte, codes are signed 8-bit integers: the value
  * is code * 2^(byte - 133), which is the MX format's INT8 (a code of 64 is 1.0).
  * The byte is the smallest in [0, 254] under which no code exceeds 127; codes
- * are rounded to nearest even and saturate at 127 (above 127 * 2^121 only).  A block
- * that holds an infinity or a NaN has byte 255 and codes 0, and stands for NaN.
+ * are rounded to nearest even and saturate at +-127 (magnitudes above 127 * 2^121 only, the
+ * lowest and the largest values of both types among them).  A block that holds an
+ * infinity or a NaN has byte 255 and codes 0, and stands for NaN.
  */
 #ifndef NVFP4_BLOCKS_H
 #define NVFP4_BLOCKS_H
