@@ -203,7 +203,7 @@ def _act_forward(gate, up, act, save):
 
 
 def _act_backward(act, kept, dy, shape, need_gate, need_up, need_y):
-    """dgate, dup, y of the kept inputs, each where it is needed."""
+    """dgate, dup, y of the kept inputs, each where it is needed, of dy's type."""
     gc, gs, uc, us = kept
     rows, cols = gc.shape
     need_up = need_up and uc is not None
@@ -259,14 +259,16 @@ class _GatedActLinear(torch.autograd.Function):
             return (None,) * 5
         shape = (*dz.shape[:-1], w.shape[1])
         dz = dz.reshape(-1, w.shape[0])
-        da = dz @ w if need_gate or need_up else dz
+        # under autocast dz has the product's type, which its other factors then take as well
+        da = (dz @ w.to(dz.dtype)).to(w.dtype) if need_gate or need_up else w
         dg, du, a = _act_backward(ctx.act, kept, da, shape, need_gate, need_up, need_w)
-        return dg, du, dz.t() @ a.view(-1, w.shape[1]) if need_w else None, None, None
+        dw = (dz.t() @ a.view(-1, w.shape[1]).to(dz.dtype)).to(w.dtype) if need_w else None
+        return dg, du, dw, None, None
 
 
 def gated_act_linear(gate, up, weight, act: str = "silu"):
-    """gated_act(gate, up, act) @ weight^T for a layer that stays in BF16 (or FP32; torch's product): the activation,
-    which the weight's gradient takes, is not kept but formed again from gate's and up's 8 bits."""
+    """gated_act(gate, up, act) @ weight^T for a layer that stays in BF16 (or FP32; torch's product, under autocast in its
+    type): the activation, which the weight's gradient takes, is not kept but formed again from gate's and up's 8 bits."""
     return _GatedActLinear.apply(gate, up, weight, _act_code(act), torch.is_grad_enabled())
 
 
