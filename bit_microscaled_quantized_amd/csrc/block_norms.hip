@@ -10,6 +10,7 @@
 // size reaches 6.2), backward 671 MB in 122 us (5.5 TB/s, with the sums over rows).
 #include "act_device.hpp"
 #include "blocks_launch.hpp"
+#include "per_device.hpp"
 #include "row_codes.hpp"
 
 namespace nvfp4 {
@@ -726,12 +727,15 @@ BackShape back_shape(int64_t rows, int64_t cols, int N) {
   return b;
 }
 
+// LDS of the backward pass's gains at most: beside it the workgroup's sums, within 160 KB.
+constexpr int kMostGains = 150 * 1024;
+
 template <typename T, int KIND>
 hipError_t norms_back_t(const NormsBackArgs& a, const BackShape& b, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
   // the gains, and a gate that is one row for all; the groups' sums meet there
   const int64_t lds = (int64_t)b.row.G * b.row.vpt * N * (KIND == kChannel ? 12 : 8);
-  if (b.row.vpt == 0 || lds > 150 * 1024) {
+  if (b.row.vpt == 0 || lds > kMostGains) {
     k_block_norms_back_wide<T, KIND><<<(unsigned)b.parts, 1024, 0, s>>>(a);
     return hipGetLastError();
   }
@@ -742,8 +746,11 @@ hipError_t norms_back_t(const NormsBackArgs& a, const BackShape& b, hipStream_t 
     auto* kernel = stream ? &k_block_norms_back<T, VPT, KIND, true, true> : &k_block_norms_back<T, VPT, KIND, false, true>;
     if constexpr (VPT == 1)
       if (b.row.G < 64) kernel = &k_block_norms_back<T, 1, KIND, false, false>;
-    if (lds > 64 * 1024)
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (lds > 64 * 1024) {
+      static std::atomic<uint64_t> done{0};
+      e = allow_lds(done, kMostGains, &k_block_norms_back<T, VPT, KIND, true, true>,
+                    &k_block_norms_back<T, VPT, KIND, false, true>);
+    }
     if (e == hipSuccess) kernel<<<(unsigned)b.parts, b.groups * b.row.G, lds, s>>>(a, b.row.G);
   });
   return e == hipSuccess ? hipGetLastError() : e;

@@ -24,4 +24,19 @@ hipError_t once_per_device(std::atomic<uint64_t>& done, F&& f) {
   return r;
 }
 
+// Allows kernels `bytes` of dynamic LDS, which beyond 64 KB they have to be: a kernel's most,
+// whatever a call takes, so that none takes away what a call of another host thread is
+// about to launch with.
+template <typename... K>
+hipError_t allow_lds(std::atomic<uint64_t>& done, int bytes, K*... kernels) {
+  return once_per_device(done, [&] {
+    hipError_t e = hipSuccess;
+    auto allow = [&](const void* f) {
+      if (e == hipSuccess) e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    (allow(reinterpret_cast<const void*>(kernels)), ...);
+    return e;
+  });
+}
+
 }  // namespace nvfp4
