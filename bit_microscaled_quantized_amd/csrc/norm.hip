@@ -14,6 +14,7 @@
 // through LDS, always in the same order.
 #include "layers_device.hpp"
 #include "layers_launch.hpp"
+#include "per_device.hpp"
 #include "rows_device.hpp"
 
 namespace nvfp4 {
@@ -600,6 +601,9 @@ BackShape back_shape(int64_t rows, int64_t cols, int N) {
   return b;
 }
 
+// LDS of a row's sums at most: 1024 lanes of eight FP32 vectors.
+constexpr int kMostSums = 128 * 1024;
+
 template <typename T>
 hipError_t norm_back_t(const NormBackArgs& a, hipStream_t s) {
   constexpr int N = VecOf<T>::N;
@@ -619,8 +623,10 @@ hipError_t norm_back_t(const NormBackArgs& a, hipStream_t s) {
     auto* kernel = stream ? &k_rms_norm_back<T, VPT, true, true> : &k_rms_norm_back<T, VPT, false, true>;
     if constexpr (VPT == 1)
       if (r.G < 64) kernel = stream ? &k_rms_norm_back<T, 1, true, false> : &k_rms_norm_back<T, 1, false, false>;
-    if (lds > 64 * 1024)
-      e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (lds > 64 * 1024) {
+      static std::atomic<uint64_t> done{0};
+      e = allow_lds(done, kMostSums, &k_rms_norm_back<T, VPT, true, true>, &k_rms_norm_back<T, VPT, false, true>);
+    }
     if (e == hipSuccess) kernel<<<(unsigned)parts, groups * r.G, lds, s>>>(a, r.G);
   });
   return e == hipSuccess ? hipGetLastError() : e;

@@ -88,7 +88,7 @@ for d in (0, 1, 0):
 """
 
 
-@pytest.mark.parametrize("name", ["block_norms"])
+@pytest.mark.parametrize("name", ["block_norms", "rms_norm"])
 def test_limits_are_set_once(tmp_path, name):
     src, lib = tmp_path / "shim.cpp", tmp_path / "libshim.so"
     src.write_text(SHIM)
