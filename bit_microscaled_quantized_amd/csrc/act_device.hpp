@@ -11,8 +11,9 @@ namespace nvfp4 {
 
 constexpr float kLog2e_act = 1.44269504088896340736f;
 
-// 1 / (1 + exp(-v)) by the hardware's 2^x and reciprocal: within 4 u + 2 |v| u, u = 2^-24
-// (the exponent's rounding, the instructions' 1 ulp each, the sum's).
+// 1 / (1 + exp(-v)) by the hardware's 2^x and reciprocal: within (5 + 1.25 |v|) u of itself, u = 2^-24 (the
+// exponent's product by a rounded log2 e, the instructions' 1 ulp each, the sum's), where it is 2^-126
+// or more.  Below, for v < -87.3, it is 0: the reciprocal has no subnormal results.
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2e_act));
 }

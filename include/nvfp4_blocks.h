@@ -13,9 +13,11 @@
  * column count and any leading dimension ld >= cols (in elements) and need their
  * element's alignment, where nothing else is said; rows * cols < 2^32, with at
  * most 2^28 - 16 rows; zero rows are no error, and sums over them are zero.
- * Arithmetic is FP32 (IEEE binary32), rounded once to the output's type.
- * Infinities and NaN are carried through as IEEE arithmetic carries them, and in
- * 8 bits as said below.  Every result is deterministic.
+ * Arithmetic is FP32 (IEEE binary32), rounded once to the output's type; the logistic
+ * function p of v, in activations and gates, is within (5 + 1.25 |v|) 2^-24 of itself, and 0
+ * where it is below 2^-126 (SiLU of v < -87.3 is -0).  Infinities and NaN are carried
+ * through as IEEE arithmetic carries them, and in 8 bits as said below.  Every result is
+ * deterministic.
  *
  * Codes with a scale per row (the product's operands).  amax = the row's largest
  * magnitude; scale = amax / 127; code = nearest even integer of v * (127 / amax),
