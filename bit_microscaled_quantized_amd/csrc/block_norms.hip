@@ -6,8 +6,9 @@
 // j + G, ..., up to VPT of them, which stay in registers over both of the row's sums
 // (and, with codes as output, its maximum); rows wider than a workgroup's registers
 // are read once per sum and once more.  Sums are FP32 in a fixed order.
-// 8192 x 5120 BF16 with a gate per row: 420 MB in 69 us (6.1 TB/s; a copy of tensors of that
-// size reaches 6.2), backward 671 MB in 122 us (5.5 TB/s, with the sums over rows).
+// 8192 x 5120 BF16 with a gate per row: 420 MB in 68 to 69 us (6.1 TB/s; a copy of tensors of that
+// size reaches 6.2), backward 671 MB in 123 to 124 us (5.4 TB/s; 120 and 5.6 without the second
+// launch, which adds the sums over rows).
 #include "act_device.hpp"
 #include "blocks_launch.hpp"
 #include "per_device.hpp"
@@ -711,7 +712,9 @@ struct BackShape {
 BackShape back_shape(int64_t rows, int64_t cols, int N) {
   BackShape b;
   b.row = row_shape((cols + N - 1) / N, 1);
-  if (b.row.vpt * N > 16 || cols < N) b.row = RowShape{0, 0};  // beyond the registers, or less than a vector
+  // Beyond the registers, or less than a vector: a workgroup for each row, which narrow rows in number
+  // pay for (2^20 x 4 BF16 39 ms; x 8, in registers, 0.18).
+  if (b.row.vpt * N > 16 || cols < N) b.row = RowShape{0, 0};
   if (b.row.vpt == 0) return BackShape{b.row, 1, std::min<int64_t>(rows, kCus)};
   // As many rows as a workgroup of 1024 lanes takes share a copy of the gains and a row of
   // sums, while that leaves a workgroup to each CU (16384 x 4096 BF16 with a gate per row

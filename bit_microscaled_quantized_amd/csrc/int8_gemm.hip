@@ -10,9 +10,9 @@
 // those behind the last full round) are split over K: the parts leave their integers in
 // the workspace, in the order of the lanes, and a second launch adds and scales them.
 //
-// Large products are bound by the chip's power (8192 x 20480 x 5120: 745 us, 2305 TOP/s; 1.5
+// Large products are bound by the chip's power (8192 x 20480 x 5120: 742 us, 2315 TOP/s; 1.5
 // times as fast on operands of zeros), products of some hundred tokens by the wait for each
-// tile's stages and by their launches (300 x 4096 x 4096 13 us).
+// tile's stages and by their launches (300 x 4096 x 4096 13.5 us, 15.5 with the weight out of the caches).
 #include "blocks_launch.hpp"
 #include "int8_device.hpp"
 #include "int8_ring.hpp"
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(TILE_THREADS) void k_int8_join(GemmArgs g) {
 }
 
 // The weight streams past the tokens: up to 16, and up to 64 where it is so large that its
-// bytes are the time (48 x 5120 x 20480 26.6 us, 28.9 in tiles; 64 x 4096 x 4096 12.7, 10.1 in
-// tiles; 48 x 8192 x 4096 14.1 and 15.5; 24 x 4096 x 4096 9.9 and 8.7).
+// bytes are the time (48 x 5120 x 20480 26.4 us, 28.8 in tiles at their best parts; 64 x 4096 x
+// 4096 13.2, 10.3 in tiles; 48 x 8192 x 4096, at the border, 14.1 and 13.2; 24 x 4096 x 4096 9.7 and 9.2).
 bool few_tokens(int64_t M, int64_t N, int64_t K) { return M <= 16 || (M <= 64 && N * K >= (int64_t(1) << 25)); }
 
 int64_t tiles_of(int64_t n, int W) { return (n + tile_side(W) - 1) / tile_side(W); }
@@ -161,10 +161,10 @@ constexpr int64_t slots_of(int W, bool ring) { return 256 * per_cu(W, ring ? kRi
 // picks takes 0.5 % longer than the best of all in the mean, 6 % at most).  A stage takes
 // longer the more of them run: of a CU's own (small tiles), of the caches and of the
 // chip's power.  At their best parts W = 4, W = 2, W = 2 in three buffers and W = 1 take, in
-// microseconds (M x N x K; 8192 x 20480 x 5120 746, 856 and more):
-//   4096 x 5120 x 20480  376 416 490 656      1024 x 20480 x 5120  129 130 145 187
-//    100 x 5120 x 20480   46  38  33  41       300 x  4096 x  4096   27  20  19  13
-//   6061 x 11072 x   512   93  72 115 103
+// microseconds (M x N x K; 8192 x 20480 x 5120 747, 842 and more):
+//   4096 x 5120 x 20480  380 422 500 677      1024 x 20480 x 5120  133 135 152 190
+//    100 x 5120 x 20480   45  37  33  41       300 x  4096 x  4096   27  21  20  13
+//   6061 x 11072 x   512   98  89 115 105
 double round_us(int64_t tiles, double stages, int W, bool ring) {
   const double full = (double)tiles / (double)slots_of(W, ring);
   if (W == 4) return stages * (1.22 + 0.41 * full) + 13.5;

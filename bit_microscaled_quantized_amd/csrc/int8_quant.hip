@@ -4,7 +4,8 @@
 // Bound by HBM: a group of lanes holds a row in registers between its largest
 // magnitude and its codes, so each input is read once; rows wider than a
 // workgroup's registers are read (and the activation formed) twice.  8192 x 5120 BF16:
-// 126 MB in 21 us (5.9 TB/s).
+// 126 MB in 24 us (5.2 TB/s) over tensors that change from call to call; 20 over the same ones, which
+// the caches hold in part, and 28 to 30 between two products of 8192 tokens.
 #include "act_device.hpp"
 #include "blocks_launch.hpp"
 #include "row_codes.hpp"
@@ -103,9 +104,10 @@ __global__ __launch_bounds__(1024) void k_int8_wide(QuantArgs a) {
   }
 }
 
-// Vectors a lane: one finishes a few rows soonest, two or (wide rows) five stream best
-// (8192 x 5120 bf16 35.8 us with one, 22.0 with two, 21.2 with five; 4096 x 5120 fp32 20.7,
-// 21.0, 18.4; 2048 x 4096 bf16 6.8, 6.1, 6.3).
+// Vectors a lane: one finishes a few rows soonest, two or (wide rows) five stream best, over tensors that
+// change (8192 x 5120 bf16 36.0 us with one, 24.1 with two, 24.0 with five; 4096 x 5120 fp32 22.0,
+// 22.1, 21.4; 2048 x 4096 bf16 8.1, 7.4, 7.7; 300 x 5120 4.5, 5.0, 4.7) as over the same ones (27.8, 20.5,
+// 20.3; 18.1, 18.4, 16.5; 6.5, 5.5, 5.6; 4.7, 4.6, 4.6).
 template <typename T, int ACT>
 hipError_t quantize_t(const QuantArgs& a, hipStream_t s) {
   const int64_t vecs = a.padded / VecOf<T>::N;
