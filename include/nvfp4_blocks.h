@@ -123,7 +123,8 @@ nvfp4_status nvfp4_block_norms(const void *x, const void *residual, const void *
  *   sum over the rows [cols] (ld_dgate unused).  dpost_gamma, dpre_gamma [cols]
  *   FP32.  Outputs may be NULL, not all of them, dgate is NULL where gate is; an
  *   output may be one of dy, dh, h, x, gate of its own size (same ld).  Sums over rows
- *   run in a fixed order.
+ *   run in a fixed order.  Rows narrower than 16 bytes take a workgroup each (2^20 rows of 4
+ *   BF16 columns 39 ms, of 8 0.18).
  *   workspace: at least nvfp4_block_norms_backward_workspace_size(rows, cols)
  *   bytes, 4-byte aligned (may be NULL where no sum over rows is asked for, or that
  *   size is 0), in use until the call's work on `stream` completes.  Fewer bytes:
